@@ -82,8 +82,9 @@ extern "C" {
  * logits before softmax and selection; NULL means no bias.  It is read by
  * every forward (the pointer is kept, the data is not copied).
  * flags: any combination of MOE_FLAG_TWO_STREAM (see the top of this file),
- * MOE_FLAG_TCGEN05, MOE_FLAG_TEST_HOLD_PANEL and MOE_FLAG_FP8_WEIGHTS
- * (below); other bits are rejected with MOE_ERR_UNSUPPORTED_SHAPE.
+ * MOE_FLAG_TCGEN05, MOE_FLAG_TEST_HOLD_PANEL, MOE_FLAG_FP8_WEIGHTS,
+ * MOE_FLAG_PARTIAL_SUM and MOE_FLAG_W4_WEIGHTS (below) that their own texts
+ * allow; other bits are rejected with MOE_ERR_UNSUPPORTED_SHAPE.
  */
 #define MOE_FLAG_TWO_STREAM 1u
 /*
@@ -133,6 +134,16 @@ extern "C" {
  * exchanged over NVLink ("Recovering time between operators").
  */
 #define MOE_FLAG_PARTIAL_SUM 16u
+/*
+ * MOE_FLAG_W4_WEIGHTS: the expert weights (routed and shared) are 4-bit codes
+ * with a scale, and optionally a zero point, per group of inputs, as laid out
+ * by moe_w4_pack, and passed to moe_decode_forward_w4 (the other forward
+ * entry points reject such a handle).  Weight-only: router and activations
+ * stay bf16.  Needs hidden, inter and shared_inter to be multiples of 64;
+ * combinable with MOE_FLAG_PARTIAL_SUM only.  The handle's workspace grows by
+ * max_batch * (top_k + n_shared) * hidden * 4 bytes.
+ */
+#define MOE_FLAG_W4_WEIGHTS 64u
 typedef struct moe_decode_shapes {
   int32_t hidden;
   int32_t n_experts;
@@ -292,6 +303,139 @@ int moe_decode_forward_fp8(moe_decode_t h, const void* x, const void* router_w, 
 #define MOE_REDUCE_MAX_PARTS 16
 int moe_decode_reduce_residual(const void* const* partials, int32_t n_parts, const void* x, void* out,
                                int32_t batch, int32_t hidden, void* stream);
+
+/* ------------------------------------------------- 4-bit weight products */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_FP16 1
+#define MOE_DTYPE_FP32 2 /* moe_balance_loss only */
+#define MOE_W4_MAX_BATCH 64
+#define MOE_W4_MAX_IN 32768
+#define MOE_W4_MAX_OUT 524288
+
+/*
+ * A 4-bit matrix W [out, in] is given by codes q (0..15), a scale s and
+ * optionally a zero point z (a whole number 0..15; 8 without them) per output
+ * and group of `group` inputs: W[n, k] = s[n, k / group] * (q[n, k] - z[n, k / group]).
+ * group: 32, 64 or 128; in: a multiple of 64 and of group, up to
+ * MOE_W4_MAX_IN; out: 1 .. MOE_W4_MAX_OUT.
+ *
+ * The products take it in a packed form, one buffer per matrix: panels of 16
+ * outputs (the last one padded), each the panel's codes -- in / 64 tiles of
+ * 512 bytes -- and then its in / group entries of scales (and zero points).
+ * A tile is 32 lanes (g = 0..7, t = 0..3; lane 4 g + t) of four 32-bit words
+ * s; bits 4 j and 16 + 4 j of a word (j = 0..3) are the codes of output
+ * g + 8 (j & 1) and of inputs 32 (s >> 1) + 8 t + 4 (s & 1) + 2 (j >> 1) and
+ * the next.  An entry is, for each g, the scales of outputs g and g + 8, and
+ * with zero points those of g and g + 8 after them, 16-bit numbers of the
+ * activations' type.
+ *
+ * moe_w4_packed_bytes: size of the packed form (0 for sizes outside the
+ * envelope).  Host only.
+ */
+uint64_t moe_w4_packed_bytes(int32_t out_features, int32_t in_features, int32_t group, int32_t has_zeros);
+
+/*
+ * Lay one matrix out (once, at load time; asynchronous on `stream`).
+ *   codes  : device uint8 [out, in / 2], input 2 j in the low and 2 j + 1 in
+ *            the high half of byte j
+ *   scales : device bf16 / fp16 [out, in / group] (dtype: MOE_DTYPE_*)
+ *   zeros  : device uint8 [out, in / group], values 0..15 (the low four bits
+ *            count), or NULL
+ *   packed : device, moe_w4_packed_bytes(...) bytes, 16-byte aligned
+ * Errors: MOE_ERR_UNSUPPORTED_SHAPE, MOE_ERR_INVALID_ARG (NULL or misaligned
+ * pointer, bad dtype), MOE_ERR_NO_DEVICE, MOE_ERR_ARCH, MOE_ERR_CUDA.
+ */
+int moe_w4_pack(const void* codes, const void* scales, const void* zeros, void* packed, int32_t out_features,
+                int32_t in_features, int32_t group, int32_t dtype, void* stream);
+
+/*
+ * out[b, n] = round(bias[n] + sum_k x[b, k] * W[n, k]), b < batch: a dense
+ * layer on a packed 4-bit matrix for 1 .. MOE_W4_MAX_BATCH tokens.  Products
+ * and sums in fp32 (no weight is rounded), one rounding to the type of x.
+ * Deterministic.  Asynchronous on `stream` of the current device, one kernel,
+ * no workspace, nothing kept between calls: calls may overlap on any streams
+ * and be captured in CUDA graphs.
+ *   x      : device [batch, in], rows x_stride elements apart (a multiple of
+ *            8; ignored for one token), 16-byte aligned
+ *   packed : device, the matrix in packed form, 16-byte aligned
+ *   bias   : device [out] or NULL
+ *   out    : device [batch, out], rows out_stride >= out elements apart;
+ *            elements between rows are not written; must not overlap x
+ *   dtype  : type of x, bias, out and of the packed scales (MOE_DTYPE_BF16 or
+ *            MOE_DTYPE_FP16); batch 0 reads and writes nothing
+ * Errors: as moe_w4_pack.
+ */
+int moe_w4_linear(const void* x, const void* packed, const void* bias, void* out, int32_t batch, int32_t in_features,
+                  int32_t out_features, int32_t group, int32_t has_zeros, int64_t x_stride, int64_t out_stride,
+                  int32_t dtype, void* stream);
+
+/*
+ * moe_decode_forward with 4-bit expert weights (a handle created with
+ * MOE_FLAG_W4_WEIGHTS).  x, router_w, out, topk_ids, topk_w and batch as for
+ * moe_decode_forward; four kernels on `stream`.
+ *   w13 : HOST array of n_experts device pointers -> packed [2 * inter, hidden]
+ *         (outputs [0, inter) the gate, [inter, 2 * inter) the up projection)
+ *   w2  : HOST array of n_experts device pointers -> packed [hidden, inter]
+ *   shared_w13, shared_w2 : device, packed (NULL iff n_shared == 0)
+ *   group, has_zeros : of every matrix; scales (and zero points) in bf16
+ * The experts' products are added in a fixed order: the outputs are the same
+ * bits on every call with the same routing weights.  Stage counters of
+ * moe_decode_stats are not kept for this path.  Errors: as
+ * moe_decode_forward; MOE_ERR_INVALID_ARG also for a handle made without
+ * MOE_FLAG_W4_WEIGHTS, MOE_ERR_UNSUPPORTED_SHAPE for a group that does not
+ * divide hidden, inter and shared_inter.
+ */
+int moe_decode_forward_w4(moe_decode_t h, const void* x, const void* router_w, const void* const* w13,
+                          const void* const* w2, const void* shared_w13, const void* shared_w2, void* out,
+                          int32_t* topk_ids, float* topk_w, int32_t batch, int32_t group, int32_t has_zeros,
+                          void* stream);
+
+/* ---------------------------------------------------- the router's balance */
+#define MOE_BALANCE_MAX_TOKENS 16777216
+
+/* Workspace bytes of moe_balance_loss for n_experts (0 outside the envelope).
+ * Host only. */
+uint64_t moe_balance_workspace_bytes(int32_t n_experts);
+
+/*
+ * The balance loss of a batch of routed tokens, the choices per expert, and
+ * the gradient with respect to the router's logits.  With p_t =
+ * softmax(logits_t + router_bias), c_e the choices of expert e by live tokens
+ * and T the live tokens:
+ *   loss           = coef * E / (top_k * T^2) * sum_e c_e * sum_t p_te
+ *   dlogits[t, e]  = grad * coef * E / (top_k * T^2) * p_te * (c_e - sum_j p_tj c_j)
+ * (coef * E * sum_e of the share of choices times the mean probability; the
+ * counts are constants to the gradient).  Without live tokens the loss and
+ * the gradient are 0.
+ *   logits      : device [tokens, n_experts] of `dtype` (MOE_DTYPE_FP32,
+ *                 _BF16 or _FP16), rows logits_stride elements apart (a
+ *                 multiple of 4), aligned to four elements; -infinity is an
+ *                 expert that cannot be chosen, a row of nothing else
+ *                 contributes to the counts alone
+ *   router_bias : device float32 [n_experts] or NULL
+ *   topk_ids    : device int32 [tokens, top_k]; an id outside
+ *                 [0, n_experts) (a dropped choice, say -1) is not counted
+ *   token_mask  : device bytes [tokens], 0: a padded token, which counts for
+ *                 nothing and whose gradient row is 0; NULL: all are live
+ *   loss        : device float32 [1]
+ *   counts      : device int32 [n_experts + 1], the last the live tokens
+ *   dlogits     : device [tokens, n_experts] of `dtype`, rows dlogits_stride
+ *                 apart, or NULL (no gradient); may be the logits' own buffer
+ *                 with the same stride
+ *   grad_loss   : device float32 [1], the loss's own gradient, or NULL (1)
+ *   workspace   : device, moe_balance_workspace_bytes(n_experts) bytes,
+ *                 16-byte aligned, of any content; two calls (or graphs) that
+ *                 may run at the same time need one each
+ * tokens 0..MOE_BALANCE_MAX_TOKENS; n_experts and top_k as moe_decode_shapes.
+ * Loss sums in fp64 over rows of fp32; the same bits on every call.
+ * Asynchronous on `stream` of the current device, one or two kernels.
+ * Errors: MOE_ERR_UNSUPPORTED_SHAPE, MOE_ERR_INVALID_ARG, MOE_ERR_NO_DEVICE,
+ * MOE_ERR_ARCH, MOE_ERR_CUDA.
+ */
+int moe_balance_loss(const void* logits, const float* router_bias, const int32_t* topk_ids, const uint8_t* token_mask,
+                     float* loss, int32_t* counts, void* dlogits, const float* grad_loss, int32_t tokens,
+                     int32_t n_experts, int32_t top_k, int64_t logits_stride, int64_t dlogits_stride, float coef,
+                     int32_t dtype, void* workspace, void* stream);
 
 /* Free the workspace and events; NULL is accepted.  Waits for the handle's
  * work first, as moe_decode_get_status does. */

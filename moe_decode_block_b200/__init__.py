@@ -36,6 +36,8 @@ EXPORTED = (
     "moe_decode_last_cuda_error", "moe_decode_last_cuda_error_string", "moe_decode_workspace_bytes",
     "moe_decode_set_timing_events", "moe_decode_set_wait_limit", "moe_router_topk_noalloc",
     "moe_router_topk_noalloc_status", "moe_decode_reduce_residual",
+    "moe_decode_forward_w4", "moe_w4_packed_bytes", "moe_w4_pack", "moe_w4_linear",
+    "moe_balance_workspace_bytes", "moe_balance_loss",
 )
 MOE_TIMING_EVENTS = 6
 MOE_FLAG_TWO_STREAM = 1
@@ -43,7 +45,11 @@ MOE_FLAG_TCGEN05 = 2
 MOE_FLAG_TEST_HOLD_PANEL = 4
 MOE_FLAG_FP8_WEIGHTS = 8
 MOE_FLAG_PARTIAL_SUM = 16
+MOE_FLAG_W4_WEIGHTS = 64
 MOE_REDUCE_MAX_PARTS = 16
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP16 = 1
+MOE_DTYPE_FP32 = 2
 
 
 class Shapes(ctypes.Structure):
@@ -118,6 +124,19 @@ def load_library() -> ctypes.CDLL:
     lib.moe_decode_reduce_residual.restype = I
     lib.moe_decode_set_wait_limit.argtypes = [P, ctypes.c_uint32]
     lib.moe_decode_set_wait_limit.restype = I
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    lib.moe_decode_forward_w4.argtypes = [P, P, P, P, P, P, P, P, P, P, i32, i32, i32, P]
+    lib.moe_decode_forward_w4.restype = I
+    lib.moe_w4_packed_bytes.argtypes = [i32, i32, i32, i32]
+    lib.moe_w4_packed_bytes.restype = ctypes.c_uint64
+    lib.moe_w4_pack.argtypes = [P, P, P, P, i32, i32, i32, i32, P]
+    lib.moe_w4_pack.restype = I
+    lib.moe_w4_linear.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, i64, i64, i32, P]
+    lib.moe_w4_linear.restype = I
+    lib.moe_balance_workspace_bytes.argtypes = [i32]
+    lib.moe_balance_workspace_bytes.restype = ctypes.c_uint64
+    lib.moe_balance_loss.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i64, i64, ctypes.c_float, i32, P, P]
+    lib.moe_balance_loss.restype = I
     lib.moe_decode_workspace_bytes.argtypes = [ctypes.POINTER(Shapes)]
     lib.moe_decode_workspace_bytes.restype = ctypes.c_uint64
     _lib = lib
@@ -143,6 +162,11 @@ def _stream_handle(s) -> Optional[int]:
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _current_stream(device=None) -> int:
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def router_topk_noalloc(x, router_w, topk_ids, topk_w, top_k: int, router_bias=None, stream=None):
@@ -189,13 +213,15 @@ class MoEDecode:
     and routed experts) and the combine on the main stream.  two_stream=True:
     MOE_FLAG_TWO_STREAM, the shared expert on the aux stream.  tcgen05=True:
     MOE_FLAG_TCGEN05, the expert kernel on tcgen05 with TMEM accumulators.
-    fp8=True: MOE_FLAG_FP8_WEIGHTS (forward_fp8).  partial=True:
+    fp8=True: MOE_FLAG_FP8_WEIGHTS (forward_fp8).  w4=True:
+    MOE_FLAG_W4_WEIGHTS (forward_w4; matrices packed with w4.py).  partial=True:
     MOE_FLAG_PARTIAL_SUM, `out` receives the fp32 expert sum without the
     residual (one tensor-parallel rank's share; see tp.py)."""
 
     def __init__(self, hidden: int, n_experts: int, top_k: int, inter: int, shared_inter: int = 0,
                  n_shared: int = 1, max_batch: int = 64, router_bias=None, two_stream: bool = False,
-                 tcgen05: bool = False, extra_flags: int = 0, fp8: bool = False, partial: bool = False):
+                 tcgen05: bool = False, extra_flags: int = 0, fp8: bool = False, partial: bool = False,
+                 w4: bool = False):
         self._lib = load_library()
         self._bias = router_bias  # keep the device tensor alive
         self.two_stream = bool(two_stream)
@@ -203,6 +229,7 @@ class MoEDecode:
         flags = (MOE_FLAG_TWO_STREAM if two_stream else 0) | (MOE_FLAG_TCGEN05 if tcgen05 else 0) | int(extra_flags)
         flags |= MOE_FLAG_FP8_WEIGHTS if fp8 else 0
         flags |= MOE_FLAG_PARTIAL_SUM if partial else 0
+        flags |= MOE_FLAG_W4_WEIGHTS if w4 else 0
         self.shapes = Shapes(hidden, n_experts, top_k, inter, shared_inter if n_shared else 0, n_shared,
                              max_batch, _ptr(router_bias), flags)
         h = ctypes.c_void_p()
@@ -268,6 +295,28 @@ class MoEDecode:
                                               _ptr(shared_w13s), _ptr(shared_w2q), _ptr(shared_w2s), _ptr(out),
                                               _ptr(topk_ids), _ptr(topk_w), int(batch), sm, sa)
         _check(rc, "moe_decode_forward_fp8")
+
+    def forward_w4(self, x, router_w, w13, w2, shared_w13, shared_w2, out, topk_ids, topk_w, group: int,
+                   zeros: bool = False, batch: Optional[int] = None, stream=None):
+        """Enqueue one forward with 4-bit expert weights (handle made with
+        w4=True): w13 / w2 [E, panels, panel bytes] uint8 (or lists of E) in
+        packed form (w4.pack), shared_w13 / shared_w2 likewise without the E
+        axis; group and zeros as the matrices were packed."""
+        if batch is None:
+            batch = x.shape[0]
+        H, I, Is = self.shapes.hidden, self.shapes.inter, self.shapes.shared_inter
+        for name, w, n, k in (("w13", w13, 2 * I, H), ("w2", w2, H, I), ("shared_w13", shared_w13, 2 * Is, H),
+                              ("shared_w2", shared_w2, H, Is)):
+            need = self._lib.moe_w4_packed_bytes(n, k, int(group), int(bool(zeros)))
+            one = w if not hasattr(w, "data_ptr") or name.startswith("shared") else w[0]
+            for t in (one if isinstance(one, (list, tuple)) else (one,)):
+                if hasattr(t, "data_ptr") and need and t.numel() * t.element_size() != need:
+                    raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes per matrix, expected {need}")
+        sm = _stream_handle(stream) if stream is not None else _current_stream()
+        rc = self._lib.moe_decode_forward_w4(self._h, _ptr(x), _ptr(router_w), self._table(w13), self._table(w2),
+                                             _ptr(shared_w13), _ptr(shared_w2), _ptr(out), _ptr(topk_ids),
+                                             _ptr(topk_w), int(batch), int(group), int(bool(zeros)), sm)
+        _check(rc, "moe_decode_forward_w4")
 
     def forward_host(self, x_host, router_w, w13, w2, shared_w13, shared_w2, out_host, ids_host, w_host,
                      batch: Optional[int] = None, stream_main=None, stream_aux=None):

@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -33,7 +34,9 @@
 #include "expert_mma.cuh"
 #include "expert_tc.cuh"
 #include "moe_device.cuh"
+#include "moe_host.h"
 #include "router_topk.cuh"
+#include "w4_experts.cuh"
 
 namespace {
 
@@ -50,7 +53,7 @@ thread_local int g_last_cuda_error = 0;
 // state never destroys them.
 struct WorkspaceLayout {
   size_t status, ticket, router_epoch, logits, plan, h, a, panel_cnt, panel_ready, queue, h_s, a_s, panel_cnt_s, panel_ready_s,
-      queue_s, acc, x_stage, out_stage, ids_stage, w_stage, state_end, maps, stage_counts, total;
+      queue_s, acc, x_stage, out_stage, ids_stage, w_stage, state_end, maps, stage_counts, w4_y, total;
 };
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -76,8 +79,13 @@ bool shapes_valid(const moe_decode_shapes* s) {
   if (s->n_shared == 1 && (!in(s->shared_inter, 8, 16384) || s->shared_inter % 8)) return false;
   if (!in(s->max_batch, 1, moe::kMaxBatch)) return false;
   if ((s->flags & ~(MOE_FLAG_TWO_STREAM | MOE_FLAG_TCGEN05 | MOE_FLAG_TEST_HOLD_PANEL | MOE_FLAG_FP8_WEIGHTS |
-                    MOE_FLAG_PARTIAL_SUM)) != 0)
+                    MOE_FLAG_PARTIAL_SUM | MOE_FLAG_W4_WEIGHTS)) != 0)
     return false;
+  if (s->flags & MOE_FLAG_W4_WEIGHTS) {
+    // 4-bit weights: whole 64-input tiles and 64-row items, their own kernels
+    if (s->hidden % 64 || s->inter % 64 || (s->n_shared && s->shared_inter % 64)) return false;
+    if (s->flags & ~(MOE_FLAG_W4_WEIGHTS | MOE_FLAG_PARTIAL_SUM)) return false;
+  }
   if (s->flags & MOE_FLAG_FP8_WEIGHTS) {
     // e4m3 weights: whole 128 x 128 scale blocks, on the mma.sync kernel
     if (s->hidden % 128 || s->inter % 128 || (s->n_shared && s->shared_inter % 128)) return false;
@@ -136,6 +144,8 @@ WorkspaceLayout layout_for(const moe_decode_shapes* s) {
   L.state_end = off;
   L.maps = take((2 * E + 2) * (size_t)moe::kTensorMapBytes);  // tensor maps: w13[E], w2[E], shared w13, w2
   L.stage_counts = take(2 * moe::kNumClasses * sizeof(unsigned long long));
+  // 4-bit weights: the products of every (token, choice), then the shared expert's
+  L.w4_y = take((s->flags & MOE_FLAG_W4_WEIGHTS) ? B * (k + (s->n_shared ? 1 : 0)) * H * 4 : 0);
   L.total = off;
   return L;
 }
@@ -435,6 +445,51 @@ int refresh_maps(moe_decode_ctx* h, const void* const* w13, const void* const* w
   return MOE_OK;
 }
 
+RouterArgs router_args(const moe_decode_ctx* h, const void* x, const void* router_w, int32_t* topk_ids, float* topk_w,
+                       int batch) {
+  const moe_decode_shapes& s = h->s;
+  RouterArgs ra{};
+  ra.x = static_cast<const __nv_bfloat16*>(x);
+  ra.router_w = static_cast<const __nv_bfloat16*>(router_w);
+  ra.bias = s.router_bias;
+  ra.B = batch;
+  ra.H = s.hidden;
+  ra.E = s.n_experts;
+  ra.k = s.top_k;
+  ra.G = router_grid(h, batch);
+  ra.chunk_rows = h->router_chunk_rows;
+  ra.logits = h->at<float>(h->L.logits);
+  ra.logits_stride = s.max_batch * s.n_experts;
+  ra.epoch = h->at<unsigned>(h->L.router_epoch);
+  ra.ticket = h->at<unsigned>(h->L.ticket);
+  ra.plan = h->at<Plan>(h->L.plan);
+  ra.topk_ids = topk_ids;
+  ra.topk_w = topk_w;
+  ra.status = h->at<int>(h->L.status);
+  ra.spin_limit = h->spin_limit;
+  return ra;
+}
+
+// Book-keeping at the end of an enqueued forward: the event that
+// get_status / get_stats / destroy wait for, and the counters.
+int finish_forward(moe_decode_ctx* h, cudaStream_t sm, int kernels, int batch) {
+  cudaError_t e;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if ((e = cudaStreamIsCapturing(sm, &cap)) != cudaSuccess) return fail_cuda(e);
+  if (cap == cudaStreamCaptureStatusNone) {
+    if ((e = cudaEventRecord(h->ev_done, sm)) != cudaSuccess) return fail_cuda(e);
+    h->done_recorded = true;
+    h->captured_last = false;
+  } else {
+    h->captured_last = true;
+  }
+  h->stats.forwards += 1;
+  h->stats.kernels_launched += (uint64_t)kernels;
+  h->stats.last_kernels = kernels;
+  h->stats.last_token_tiles = ((batch < moe::kMaxUnitTokens ? batch : moe::kMaxUnitTokens) + 7) / 8;
+  return MOE_OK;
+}
+
 // Enqueue the whole forward (device pointers only).
 int enqueue_forward(moe_decode_ctx* h, const void* x, const void* router_w, const void* const* w13,
                     const void* const* w2, const void* shared_w13, const void* shared_w2, void* out,
@@ -522,25 +577,7 @@ int enqueue_forward(moe_decode_ctx* h, const void* x, const void* router_w, cons
   base.hold_panel = ((s.flags & MOE_FLAG_TEST_HOLD_PANEL) && h->stats.forwards == 0) ? 0 : -1;
 
   // Router + top-k + plan.
-  RouterArgs ra{};
-  ra.x = static_cast<const __nv_bfloat16*>(x);
-  ra.router_w = static_cast<const __nv_bfloat16*>(router_w);
-  ra.bias = s.router_bias;
-  ra.B = batch;
-  ra.H = s.hidden;
-  ra.E = s.n_experts;
-  ra.k = s.top_k;
-  ra.G = router_grid(h, batch);
-  ra.chunk_rows = h->router_chunk_rows;
-  ra.logits = h->at<float>(h->L.logits);
-  ra.logits_stride = s.max_batch * s.n_experts;
-  ra.epoch = h->at<unsigned>(h->L.router_epoch);
-  ra.ticket = h->at<unsigned>(h->L.ticket);
-  ra.plan = h->at<Plan>(h->L.plan);
-  ra.topk_ids = topk_ids;
-  ra.topk_w = topk_w;
-  ra.status = status;
-  ra.spin_limit = h->spin_limit;
+  const RouterArgs ra = router_args(h, x, router_w, topk_ids, topk_w, batch);
   auto launch_router = [&]() -> cudaError_t {
     cudaError_t err = mark(0, sm);
     if (err != cudaSuccess) return err;
@@ -629,22 +666,131 @@ int enqueue_forward(moe_decode_ctx* h, const void* x, const void* router_w, cons
     if ((e = launch_combine(!fork)) != cudaSuccess) return bail(e);
   }
 
-  {
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if ((e = cudaStreamIsCapturing(sm, &cap)) != cudaSuccess) return fail_cuda(e);
-    if (cap == cudaStreamCaptureStatusNone) {
-      if ((e = cudaEventRecord(h->ev_done, sm)) != cudaSuccess) return fail_cuda(e);
-      h->done_recorded = true;
-      h->captured_last = false;
-    } else {
-      h->captured_last = true;
+  return finish_forward(h, sm, kernels, batch);
+}
+
+// ---- 4-bit expert weights -------------------------------------------------
+
+using W4Kernel = void (*)(moe::W4ExpertArgs, ExpertTable);
+struct W4Pick {
+  W4Kernel kern;
+  int smem, ctas;  // dynamic shared memory, CTAs per SM
+};
+template <int NT, bool DOWN>
+W4Pick pick_w4_nt(bool half_tile, bool zeros) {
+  if (half_tile && zeros) return {moe::w4_expert_kernel<NT, true, true, DOWN>, moe::W4Cfg<NT, true, true>::kSmem, moe::W4Cfg<NT, true, true>::kMinCtas};
+  if (half_tile) return {moe::w4_expert_kernel<NT, true, false, DOWN>, moe::W4Cfg<NT, true, false>::kSmem, moe::W4Cfg<NT, true, false>::kMinCtas};
+  if (zeros) return {moe::w4_expert_kernel<NT, false, true, DOWN>, moe::W4Cfg<NT, false, true>::kSmem, moe::W4Cfg<NT, false, true>::kMinCtas};
+  return {moe::w4_expert_kernel<NT, false, false, DOWN>, moe::W4Cfg<NT, false, false>::kSmem, moe::W4Cfg<NT, false, false>::kMinCtas};
+}
+// The instance for the tokens that a unit can have at this batch.
+template <bool DOWN>
+W4Pick pick_w4(int batch, bool half_tile, bool zeros) {
+  if (batch <= 8) return pick_w4_nt<1, DOWN>(half_tile, zeros);
+  if (batch <= 16) return pick_w4_nt<2, DOWN>(half_tile, zeros);
+  return pick_w4_nt<4, DOWN>(half_tile, zeros);
+}
+
+int set_w4_attrs() {
+  cudaError_t e;
+  for (int batch : {8, 16, 32})
+    for (int v = 0; v < 4; ++v) {
+      const W4Pick up = pick_w4<false>(batch, v & 1, v & 2), down = pick_w4<true>(batch, v & 1, v & 2);
+      if ((e = raise_smem_limit(up.kern, up.smem)) != cudaSuccess) return fail_cuda(e);
+      if ((e = raise_smem_limit(down.kern, down.smem)) != cudaSuccess) return fail_cuda(e);
     }
-  }
-  h->stats.forwards += 1;
-  h->stats.kernels_launched += (uint64_t)kernels;
-  h->stats.last_kernels = kernels;
-  h->stats.last_token_tiles = ((batch < moe::kMaxUnitTokens ? batch : moe::kMaxUnitTokens) + 7) / 8;
   return MOE_OK;
+}
+
+moe::W4Geom w4_geom(int k, int group, bool zeros) {
+  moe::W4Geom g{};
+  g.tiles = k / moe::kW4Tile;
+  g.panel_bytes = (uint32_t)moe::w4_panel_bytes(k, group, zeros);
+  g.entry_off = (uint32_t)(g.tiles * moe::kW4TileBytes);
+  g.group_shift = group == 128 ? 1 : 0;
+  return g;
+}
+
+// The forward on 4-bit weights: router, up + SwiGLU, down, combine.
+int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, const void* const* w13,
+                       const void* const* w2, const void* shared_w13, const void* shared_w2, void* out,
+                       int32_t* topk_ids, float* topk_w, int batch, int group, bool zeros, cudaStream_t sm) {
+  const moe_decode_shapes& s = h->s;
+  cudaError_t e;
+  if (h->dirty) {
+    if ((e = cudaMemsetAsync(h->ws, 0, h->L.state_end, sm)) != cudaSuccess) return fail_cuda(e);
+    h->dirty = false;
+  }
+  for (int i = 0; i < s.n_experts; ++i) {
+    h->tab13->p[i] = static_cast<const __nv_bfloat16*>(w13[i]);
+    h->tab2->p[i] = static_cast<const __nv_bfloat16*>(w2[i]);
+  }
+  auto bail = [&](cudaError_t err) {
+    h->dirty = true;
+    return fail_cuda(err);
+  };
+  auto mark = [&](int i) { return h->timing ? cudaEventRecord(h->tev[i], sm) : cudaSuccess; };
+
+  float* y = h->at<float>(h->L.w4_y);
+  float* y_s = y + (size_t)batch * s.top_k * s.hidden;
+  moe::W4ExpertArgs up{}, down{};
+  up.n_su = down.n_su = shared_units(s, batch);
+  up.batch = down.batch = batch;
+  up.top_k = down.top_k = s.top_k;
+  up.plan = down.plan = h->at<Plan>(h->L.plan);
+  up.shared_w = static_cast<const uint8_t*>(shared_w13);
+  down.shared_w = static_cast<const uint8_t*>(shared_w2);
+  for (int ph = 0; ph < 2; ++ph) {
+    const int I = ph ? s.inter : (s.n_shared ? s.shared_inter : 64);
+    __nv_bfloat16* act = ph ? h->at<__nv_bfloat16>(h->L.a) : h->at<__nv_bfloat16>(h->L.a_s);
+    moe::W4Phase& u = up.ph[ph];
+    u.geom = w4_geom(s.hidden, group, zeros);
+    u.blocks = 2 * I / moe::kW4Rows;
+    u.up_off = (uint32_t)(I / 16) * u.geom.panel_bytes;
+    u.x = static_cast<const __nv_bfloat16*>(x);
+    u.x_cols = s.hidden;
+    u.out = act;
+    u.out_cols = I;
+    moe::W4Phase& d = down.ph[ph];
+    d.geom = w4_geom(I, group, zeros);
+    d.blocks = s.hidden / moe::kW4Rows;
+    d.x = act;
+    d.x_cols = I;
+    d.out = ph ? y : y_s;
+    d.out_cols = s.hidden;
+  }
+  // persistent grids: every resident CTA, but no more than there can be items
+  const int most_units = (batch * s.top_k < s.n_experts ? batch * s.top_k : s.n_experts) +
+                         batch * s.top_k / moe::kMaxUnitTokens;
+  auto grid_for = [&](const moe::W4ExpertArgs& g, int ctas) {
+    const long long items = (long long)g.n_su * g.ph[0].blocks + (long long)most_units * g.ph[1].blocks;
+    const long long cap = (long long)ctas * h->num_sms;
+    return (int)(items < cap ? items : cap);
+  };
+  const W4Pick ku = pick_w4<false>(batch, group == 32, zeros), kd = pick_w4<true>(batch, group == 32, zeros);
+
+  if ((e = mark(0)) != cudaSuccess) return bail(e);
+  const RouterArgs ra = router_args(h, x, router_w, topk_ids, topk_w, batch);
+  e = launch(pick_router(s.n_experts), ra.G, router_threads_for(s.n_experts),
+             moe::router_smem_bytes(batch, s.n_experts, h->router_chunk_rows), sm, true, ra);
+  if (e != cudaSuccess) return bail(e);
+  if ((e = mark(1)) != cudaSuccess || (e = mark(4)) != cudaSuccess) return bail(e);
+  e = launch(ku.kern, grid_for(up, ku.ctas), moe::kW4Threads, ku.smem, sm, true, up, *h->tab13);
+  if (e != cudaSuccess) return bail(e);
+  e = launch(kd.kern, grid_for(down, kd.ctas), moe::kW4Threads, kd.smem, sm, true, down, *h->tab2);
+  if (e != cudaSuccess) return bail(e);
+  if ((e = mark(2)) != cudaSuccess || (e = mark(5)) != cudaSuccess) return bail(e);
+  const int cgrid = ceil_div(batch * s.hidden / 4, 256);
+  const auto xb = static_cast<const __nv_bfloat16*>(x);
+  const float* ys = s.n_shared ? y_s : nullptr;
+  e = (s.flags & MOE_FLAG_PARTIAL_SUM)
+          ? launch(moe::w4_combine_kernel<true>, cgrid, 256, 0, sm, true, xb, (const float*)y, ys, out, batch,
+                   (int)s.hidden, (int)s.top_k)
+          : launch(moe::w4_combine_kernel<false>, cgrid, 256, 0, sm, true, xb, (const float*)y, ys, out, batch,
+                   (int)s.hidden, (int)s.top_k);
+  if (e != cudaSuccess) return bail(e);
+  if ((e = mark(3)) != cudaSuccess) return bail(e);
+  return finish_forward(h, sm, 4, batch);
 }
 
 int check_forward_args(moe_decode_ctx* h, const void* x, const void* router_w, const void* const* w13,
@@ -859,6 +1005,38 @@ int noalloc_setup(int dev, NoAllocDevice** out) {
 
 }  // namespace
 
+namespace moe {
+
+int host_fail_cuda(cudaError_t e) { return fail_cuda(e); }
+
+int host_current_device(int* dev, int* num_sms) {
+  static std::atomic<int> sms[kHostMaxDevices];  // 0: not looked at yet
+  int n = 0;
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess || *dev < 0 || *dev >= kHostMaxDevices) {
+    g_last_cuda_error = (int)e;
+    cudaGetLastError();
+    return MOE_ERR_NO_DEVICE;
+  }
+  n = sms[*dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    int major = 0;
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev)) != cudaSuccess) {
+      cudaGetLastError();
+      g_last_cuda_error = (int)e;
+      return e == cudaErrorNoDevice || e == cudaErrorInsufficientDriver || e == cudaErrorInvalidDevice ? MOE_ERR_NO_DEVICE
+                                                                                                       : MOE_ERR_CUDA;
+    }
+    if (major != 10) return MOE_ERR_ARCH;
+    sms[*dev].store(n, std::memory_order_relaxed);
+  }
+  *num_sms = n;
+  return MOE_OK;
+}
+
+}  // namespace moe
+
 extern "C" {
 
 int moe_router_topk_noalloc(const void* x, const void* router_w, const float* router_bias, int32_t* topk_ids,
@@ -1020,7 +1198,7 @@ int moe_decode_init(const moe_decode_shapes* shapes, moe_decode_t* out_handle) {
     const bool shapes_ok = shapes->hidden % moe::kChunkCols == 0 && shapes->inter % moe::kChunkCols == 0 &&
                            (!shapes->n_shared || shapes->shared_inter % moe::kChunkCols == 0);
     uint8_t probe[moe::kTensorMapBytes];
-    h->use_tmap = env_int("MOE_DECODE_TMAP", 1, 0, 1) == 1 && shapes_ok &&
+    h->use_tmap = !(shapes->flags & MOE_FLAG_W4_WEIGHTS) && env_int("MOE_DECODE_TMAP", 1, 0, 1) == 1 && shapes_ok &&
                   encode_matrix_map(probe, h->ws, shapes->hidden, 2 * shapes->inter);
     h->use_tc = h->use_tmap && (shapes->flags & MOE_FLAG_TCGEN05) != 0;
     if (h->use_tmap) {
@@ -1031,6 +1209,7 @@ int moe_decode_init(const moe_decode_shapes* shapes, moe_decode_t* out_handle) {
     }
   }
   if (rc == MOE_OK) rc = set_kernel_attrs(h);
+  if (rc == MOE_OK && (shapes->flags & MOE_FLAG_W4_WEIGHTS)) rc = set_w4_attrs();
   if (rc != MOE_OK) {
     moe_decode_destroy(h);
     return rc;
@@ -1048,6 +1227,7 @@ int moe_decode_forward(moe_decode_t h, const void* x, const void* router_w, cons
   DeviceGuard guard(h->device);
   if (!guard.ok) return fail_cuda(cudaGetLastError());
   if (h->s.flags & MOE_FLAG_FP8_WEIGHTS) return MOE_ERR_INVALID_ARG;  // moe_decode_forward_fp8
+  if (h->s.flags & MOE_FLAG_W4_WEIGHTS) return MOE_ERR_INVALID_ARG;   // moe_decode_forward_w4
   return enqueue_forward(h, x, router_w, w13, w2, shared_w13, shared_w2, out, topk_ids, topk_w, batch,
                          static_cast<cudaStream_t>(stream_main), static_cast<cudaStream_t>(stream_aux), nullptr);
 }
@@ -1073,11 +1253,28 @@ int moe_decode_forward_fp8(moe_decode_t h, const void* x, const void* router_w, 
                          static_cast<cudaStream_t>(stream_main), static_cast<cudaStream_t>(stream_aux), &f8);
 }
 
+int moe_decode_forward_w4(moe_decode_t h, const void* x, const void* router_w, const void* const* w13,
+                          const void* const* w2, const void* shared_w13, const void* shared_w2, void* out,
+                          int32_t* topk_ids, float* topk_w, int32_t batch, int32_t group, int32_t has_zeros,
+                          void* stream) {
+  if (!h || !(h->s.flags & MOE_FLAG_W4_WEIGHTS)) return MOE_ERR_INVALID_ARG;
+  const moe_decode_shapes& s = h->s;
+  if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (s.hidden % group || s.inter % group || (s.n_shared && s.shared_inter % group)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  int rc = check_forward_args(h, x, router_w, w13, w2, shared_w13, shared_w2, out, topk_ids, topk_w, batch, true);
+  if (rc != MOE_OK) return rc;
+  if (batch == 0) return MOE_OK;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return fail_cuda(cudaGetLastError());
+  return enqueue_forward_w4(h, x, router_w, w13, w2, shared_w13, shared_w2, out, topk_ids, topk_w, batch, group,
+                            has_zeros != 0, static_cast<cudaStream_t>(stream));
+}
+
 int moe_decode_forward_host(moe_decode_t h, const void* x_host, const void* router_w, const void* const* w13,
                             const void* const* w2, const void* shared_w13, const void* shared_w2,
                             void* out_host, int32_t* ids_host, float* w_host, int32_t batch, void* stream_main,
                             void* stream_aux) {
-  if (h && (h->s.flags & MOE_FLAG_FP8_WEIGHTS)) return MOE_ERR_INVALID_ARG;  // bf16 weights only
+  if (h && (h->s.flags & (MOE_FLAG_FP8_WEIGHTS | MOE_FLAG_W4_WEIGHTS))) return MOE_ERR_INVALID_ARG;  // bf16 weights only
   if (h && (h->s.flags & MOE_FLAG_PARTIAL_SUM)) return MOE_ERR_INVALID_ARG;  // bf16 out only
   int rc = check_forward_args(h, x_host, router_w, w13, w2, shared_w13, shared_w2, out_host, ids_host, w_host,
                               batch, false);

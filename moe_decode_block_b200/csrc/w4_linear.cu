@@ -1,0 +1,272 @@
+// w4_linear.cu -- the dense layer on 4-bit weights (moe_w4_linear) and the
+// one-time layout of a matrix (moe_w4_pack).
+#include <cooperative_groups.h>
+
+#include <atomic>
+
+#include "moe_host.h"
+#include "w4_core.cuh"
+
+namespace moe {
+
+namespace cg = cooperative_groups;
+
+struct W4LinearArgs {
+  const void* x;
+  const uint8_t* w;
+  const void* bias;  // or nullptr
+  void* out;
+  int batch, n_out, n_panels;
+  W4Geom geom;
+  long long x_stride, out_stride;  // elements between tokens
+};
+
+// One CTA: kW4Rows outputs x NT * 8 tokens x its share of K; the 8 warps split
+// that share, and the CTAs of a cluster split K between them, so a matrix with
+// few outputs still fills the GPU.  The partial sums are added in a fixed
+// order: warps first, then the cluster's CTAs through distributed shared
+// memory.  Nothing is kept in global memory between calls.
+template <typename T, int NT, bool HALF, bool ZP>
+__global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, HALF, ZP>::kMinCtas)
+    w4_linear_kernel(const __grid_constant__ W4LinearArgs a) {
+  using C = W4Cfg<NT, HALF, ZP>;
+  extern __shared__ __align__(1024) uint8_t w4_smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* ring = w4_smem + (size_t)warp * C::kDepth * C::kSlot;
+  float* red = reinterpret_cast<float*>(w4_smem + (size_t)kW4Warps * C::kDepth * C::kSlot);
+
+  cg::cluster_group cluster = cg::this_cluster();
+  const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int row_blk = blockIdx.x / S;
+  const int tok0 = blockIdx.y * NT * 8;
+  const int n_tok = min(NT * 8, a.batch - tok0);
+  const int n_tok_tiles = (n_tok + 7) / 8;
+
+  const int q = rank * kW4Warps + warp, Q = S * kW4Warps;
+  const int t0 = (int)((long long)a.geom.tiles * q / Q), t1 = (int)((long long)a.geom.tiles * (q + 1) / Q);
+
+  const uint8_t* panel[kW4Panels];
+  uint32_t valid = 0;
+#pragma unroll
+  for (int m = 0; m < kW4Panels; ++m) {
+    const int p = row_blk * kW4Panels + m;
+    panel[m] = a.w + (size_t)(p < a.n_panels ? p : 0) * a.geom.panel_bytes;
+    valid |= p < a.n_panels ? 1u << m : 0u;
+  }
+  const T* xp[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int t = n * 8 + (lane >> 2);
+    xp[n] = t < n_tok ? static_cast<const T*>(a.x) + (tok0 + t) * a.x_stride + 8 * (lane & 3) : nullptr;
+  }
+
+  const uint32_t ring_addr = smem_addr(ring);
+#pragma unroll
+  for (int d = 0; d < C::kDepth - 1; ++d) {
+    if (t0 + d < t1) w4_issue<C>(ring_addr + d * C::kSlot, panel, valid, a.geom, t0 + d, lane);
+    cp_async_commit();
+  }
+  float acc[kW4Panels][NT][4] = {};
+  uint4 xr[NT][2], xn[NT][2];
+  if (t0 < t1) w4_load_x<T, NT>(xp, t0, xn);
+  int slot = 0;
+  for (int t = t0; t < t1; ++t) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      xr[n][0] = xn[n][0];
+      xr[n][1] = xn[n][1];
+    }
+    if (t + 1 < t1) w4_load_x<T, NT>(xp, t + 1, xn);
+    cp_async_wait<C::kDepth - 2>();
+    {
+      // the slot read in the last iteration takes the tile kDepth - 1 ahead
+      const int ahead = slot == 0 ? C::kDepth - 1 : slot - 1;
+      if (t + C::kDepth - 1 < t1)
+        w4_issue<C>(ring_addr + ahead * C::kSlot, panel, valid, a.geom, t + C::kDepth - 1, lane);
+      cp_async_commit();
+    }
+    w4_tile<T, NT, HALF, ZP>(ring + slot * C::kSlot, xr, n_tok_tiles, lane, acc);
+    slot = slot + 1 == C::kDepth ? 0 : slot + 1;
+  }
+  w4_store_partials<NT>(red, warp, lane, n_tok_tiles, acc);
+  __syncthreads();
+
+  const int row0 = row_blk * kW4Rows;
+  auto store = [&](int tok, int row, float v) {
+    const int n = row0 + row;
+    if (n >= a.n_out) return;
+    if (a.bias) v += W4Type<T>::to_f32(static_cast<const T*>(a.bias)[n]);
+    static_cast<T*>(a.out)[(tok0 + tok) * a.out_stride + n] = W4Type<T>::from_f32(v);
+  };
+  if (S == 1) {
+    for (int i = tid; i < n_tok * kW4Rows; i += kW4Threads) {
+      const int tok = i / kW4Rows, row = i % kW4Rows;
+      store(tok, row, w4_sum_partials<NT>(red, tok, row));
+    }
+    return;
+  }
+  // this CTA's sum replaces warp 0's partial (each element read and written
+  // by one thread), then every CTA of the cluster adds a share of them
+  for (int i = tid; i < n_tok * kW4Rows; i += kW4Threads) {
+    const int tok = i / kW4Rows, row = i % kW4Rows;
+    const float v = w4_sum_partials<NT>(red, tok, row);
+    red[tok * kW4RedPitch + row] = v;
+  }
+  cluster.sync();
+  for (int i = rank * kW4Threads + tid; i < n_tok * kW4Rows; i += S * kW4Threads) {
+    const int tok = i / kW4Rows, row = i % kW4Rows;
+    float v = 0.f;
+    for (int r = 0; r < S; ++r) v += cluster.map_shared_rank(red, r)[tok * kW4RedPitch + row];
+    store(tok, row, v);
+  }
+  cluster.sync();  // no CTA leaves while another reads its sums
+}
+
+// Plain codes to the packed layout: a thread builds one 32-bit word, another
+// range of threads the group entries.  Outputs behind the last one get codes,
+// scales and zero points of 0.
+template <typename T>
+__global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* codes, const T* scales, const uint8_t* zeros,
+                                                      uint8_t* packed, int n_out, int k, int group) {
+  const int tiles = k / kW4Tile, groups = k / group;
+  const bool zp = zeros != nullptr;
+  const size_t panel_bytes = w4_panel_bytes(k, group, zp);
+  const int p = blockIdx.y;
+  uint8_t* out = packed + (size_t)p * panel_bytes;
+  const int words = tiles * 128;
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < words + groups * 16; i += gridDim.x * blockDim.x) {
+    if (i < words) {
+      const int tile = i >> 7, lane = (i >> 2) & 31, s = i & 3;
+      const int g = lane >> 2, t = lane & 3;
+      const int in = tile * kW4Tile + 32 * (s >> 1) + 8 * t + 4 * (s & 1);
+      uint32_t w = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = p * 16 + g + 8 * (j & 1);
+        const uint32_t b = n < n_out ? codes[(size_t)n * (k / 2) + in / 2 + (j >> 1)] : 0u;
+        w |= (b & 15u) << (4 * j) | (b >> 4) << (16 + 4 * j);
+      }
+      reinterpret_cast<uint32_t*>(out)[i] = w;
+    } else {
+      const int r = i - words, grp = r >> 4, g = (r >> 1) & 7, hi = r & 1;
+      const int n = p * 16 + g + 8 * hi;
+      T* ent = reinterpret_cast<T*>(out + (size_t)tiles * kW4TileBytes) + (size_t)grp * (zp ? 32 : 16) + g * (zp ? 4 : 2);
+      ent[hi] = n < n_out ? scales[(size_t)n * groups + grp] : W4Type<T>::from_f32(0.f);
+      if (zp) ent[2 + hi] = W4Type<T>::from_f32(n < n_out ? (float)(zeros[(size_t)n * groups + grp] & 15) : 0.f);
+    }
+  }
+}
+
+namespace {
+
+bool w4_shape_ok(int n_out, int k, int group) {
+  if (n_out < 1 || n_out > MOE_W4_MAX_OUT || k < kW4Tile || k > MOE_W4_MAX_IN || k % kW4Tile) return false;
+  return (group == 32 || group == 64 || group == 128) && k % group == 0;
+}
+
+bool dtype_ok(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP16; }
+
+// Cluster size (CTAs that split K): as many as fill two CTAs on every SM, as
+// long as every warp keeps two tiles of its own.
+int cluster_for(int row_blocks, int tiles, int slots) {
+  int s = 1;
+  while (s < 8 && 2 * s * row_blocks <= slots && tiles >= 2 * s * kW4Warps * 2) s *= 2;
+  return s;
+}
+
+template <typename T, int NT, bool HALF, bool ZP>
+int launch_linear(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) {
+  using C = W4Cfg<NT, HALF, ZP>;
+  static std::atomic<uint64_t> raised{0};
+  const auto kern = w4_linear_kernel<T, NT, HALF, ZP>;
+  const int rc = host_raise_smem(kern, C::kSmem, dev, raised);
+  if (rc != MOE_OK) return rc;
+  const int row_blocks = (a.n_panels + kW4Panels - 1) / kW4Panels;
+  const int tok_blocks = (a.batch + NT * 8 - 1) / (NT * 8);
+  const int s = cluster_for(row_blocks * tok_blocks, a.geom.tiles, C::kMinCtas * num_sms);
+  const cudaError_t e =
+      host_launch(kern, dim3((unsigned)(row_blocks * s), (unsigned)tok_blocks), kW4Threads, C::kSmem, st, s, false, a);
+  return e == cudaSuccess ? MOE_OK : host_fail_cuda(e);
+}
+
+template <typename T, bool HALF, bool ZP>
+int pick_nt(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) {
+  if (a.batch <= 8) return launch_linear<T, 1, HALF, ZP>(a, dev, num_sms, st);
+  if (a.batch <= 16) return launch_linear<T, 2, HALF, ZP>(a, dev, num_sms, st);
+  return launch_linear<T, 4, HALF, ZP>(a, dev, num_sms, st);
+}
+
+template <typename T>
+int pick_linear(const W4LinearArgs& a, bool half_tile, bool zeros, int dev, int num_sms, cudaStream_t st) {
+  if (half_tile) return zeros ? pick_nt<T, true, true>(a, dev, num_sms, st) : pick_nt<T, true, false>(a, dev, num_sms, st);
+  return zeros ? pick_nt<T, false, true>(a, dev, num_sms, st) : pick_nt<T, false, false>(a, dev, num_sms, st);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+uint64_t moe_w4_packed_bytes(int32_t out_features, int32_t in_features, int32_t group, int32_t has_zeros) {
+  if (!moe::w4_shape_ok(out_features, in_features, group)) return 0;
+  return moe::w4_matrix_bytes(out_features, in_features, group, has_zeros != 0);
+}
+
+int moe_w4_pack(const void* codes, const void* scales, const void* zeros, void* packed, int32_t out_features,
+                int32_t in_features, int32_t group, int32_t dtype, void* stream) {
+  using namespace moe;
+  if (!w4_shape_ok(out_features, in_features, group)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!dtype_ok(dtype) || !codes || !scales || !packed) return MOE_ERR_INVALID_ARG;
+  if (!host_aligned(scales, 2) || !host_aligned(packed, 16)) return MOE_ERR_INVALID_ARG;
+  int dev, sms;
+  const int rc = host_current_device(&dev, &sms);
+  if (rc != MOE_OK) return rc;
+  const int items = in_features / kW4Tile * 128 + in_features / group * 16;
+  const dim3 grid((unsigned)((items + 255) / 256), (unsigned)((out_features + 15) / 16));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      dtype == MOE_DTYPE_BF16
+          ? host_launch(w4_pack_kernel<__nv_bfloat16>, grid, 256, 0, st, 1, false, static_cast<const uint8_t*>(codes),
+                        static_cast<const __nv_bfloat16*>(scales), static_cast<const uint8_t*>(zeros),
+                        static_cast<uint8_t*>(packed), (int)out_features, (int)in_features, (int)group)
+          : host_launch(w4_pack_kernel<__half>, grid, 256, 0, st, 1, false, static_cast<const uint8_t*>(codes),
+                        static_cast<const __half*>(scales), static_cast<const uint8_t*>(zeros),
+                        static_cast<uint8_t*>(packed), (int)out_features, (int)in_features, (int)group);
+  return e == cudaSuccess ? MOE_OK : host_fail_cuda(e);
+}
+
+int moe_w4_linear(const void* x, const void* packed, const void* bias, void* out, int32_t batch, int32_t in_features,
+                  int32_t out_features, int32_t group, int32_t has_zeros, int64_t x_stride, int64_t out_stride,
+                  int32_t dtype, void* stream) {
+  using namespace moe;
+  if (!w4_shape_ok(out_features, in_features, group) || batch < 0 || batch > MOE_W4_MAX_BATCH)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+  if (batch == 0) return MOE_OK;
+  if (!x || !packed || !out) return MOE_ERR_INVALID_ARG;
+  if (!host_aligned(x, 16) || !host_aligned(packed, 16) || !host_aligned(out, 2) || !host_aligned(bias, 2))
+    return MOE_ERR_INVALID_ARG;
+  if (batch > 1 && (x_stride % 8 || x_stride < 0 || out_stride < out_features)) return MOE_ERR_INVALID_ARG;
+  int dev, sms;
+  const int rc = host_current_device(&dev, &sms);
+  if (rc != MOE_OK) return rc;
+  W4LinearArgs a{};
+  a.x = x;
+  a.w = static_cast<const uint8_t*>(packed);
+  a.bias = bias;
+  a.out = out;
+  a.batch = batch;
+  a.n_out = out_features;
+  a.n_panels = (out_features + 15) / 16;
+  a.geom.tiles = in_features / kW4Tile;
+  a.geom.panel_bytes = (uint32_t)w4_panel_bytes(in_features, group, has_zeros != 0);
+  a.geom.entry_off = (uint32_t)(a.geom.tiles * kW4TileBytes);
+  a.geom.group_shift = group == 128 ? 1 : 0;
+  a.x_stride = x_stride;
+  a.out_stride = out_stride;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return dtype == MOE_DTYPE_BF16 ? pick_linear<__nv_bfloat16>(a, group == 32, has_zeros != 0, dev, sms, st)
+                                 : pick_linear<__half>(a, group == 32, has_zeros != 0, dev, sms, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,107 @@
+"""Products with 4-bit weights (a scale, and optionally a zero point, per group
+of inputs): argument marshalling of moe_w4_pack and moe_w4_linear.
+
+    packed = w4.pack(codes, scales, zeros)          # once, at load time
+    w4.linear(x, packed, out, group=128, zeros=True)
+
+The block's experts take the same packed matrices: MoEDecode(..., w4=True)
+and its forward_w4.
+"""
+from __future__ import annotations
+
+from contextlib import nullcontext
+from typing import Optional
+
+from . import MOE_DTYPE_BF16, MOE_DTYPE_FP16, _check, _current_stream, _ptr, _stream_handle, load_library
+
+MAX_BATCH = 64
+
+
+def _dtype_code(t) -> int:
+    import torch
+    if t.dtype is torch.bfloat16:
+        return MOE_DTYPE_BF16
+    if t.dtype is torch.float16:
+        return MOE_DTYPE_FP16
+    raise ValueError(f"expected bfloat16 or float16, got {t.dtype}")
+
+
+def _on(device):
+    """Make `device` current where it is not (the library launches on the
+    current device)."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {device}")
+    return nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def packed_bytes(out_features: int, in_features: int, group: int, zeros: bool = False) -> int:
+    """Bytes of a packed [out_features, in_features] matrix."""
+    n = load_library().moe_w4_packed_bytes(int(out_features), int(in_features), int(group), int(bool(zeros)))
+    if n == 0:
+        raise ValueError(f"no packed form for [{out_features}, {in_features}] in groups of {group}")
+    return n
+
+
+def pack(codes, scales, zeros=None, out=None, stream=None):
+    """Lay matrices out for the products: codes [..., N, K / 2] uint8 (input
+    2 j in the low half of byte j), scales [..., N, K / group] bfloat16 or
+    float16, zeros [..., N, K / group] uint8 or None -> uint8
+    [..., ceil(N / 16), panel bytes].  Leading axes (experts) are packed one
+    matrix at a time."""
+    import torch
+    lib = load_library()
+    if codes.dtype is not torch.uint8 or codes.dim() < 2 or not codes.is_cuda:
+        raise ValueError("codes: expected a uint8 [..., N, K / 2] tensor on the GPU")
+    n, k = codes.shape[-2], codes.shape[-1] * 2
+    if scales.shape[:-1] != codes.shape[:-1] or scales.shape[-1] < 1 or k % scales.shape[-1]:
+        raise ValueError(f"scales {tuple(scales.shape)} do not fit codes {tuple(codes.shape)}")
+    group = k // scales.shape[-1]
+    if zeros is not None and (zeros.dtype is not torch.uint8 or zeros.shape != scales.shape):
+        raise ValueError("zeros: expected uint8 of the scales' shape")
+    for name, t in (("codes", codes), ("scales", scales), ("zeros", zeros)):
+        if t is not None and (not t.is_contiguous() or t.device != codes.device):
+            raise ValueError(f"{name}: expected a contiguous tensor on {codes.device}")
+    code = _dtype_code(scales)
+    one = packed_bytes(n, k, group, zeros is not None)
+    shape = (*codes.shape[:-2], -(-n // 16), one // -(-n // 16))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.uint8, device=codes.device)
+    elif out.shape != shape or out.dtype is not torch.uint8 or not out.is_contiguous() or out.device != codes.device:
+        raise ValueError(f"out: expected a contiguous uint8 {shape} tensor on {codes.device}")
+    with _on(codes.device):
+        sm = _stream_handle(stream) if stream is not None else _current_stream()
+        for m in range(codes[..., 0, 0].numel()):
+            z = None if zeros is None else zeros.data_ptr() + m * n * (k // group)
+            rc = lib.moe_w4_pack(codes.data_ptr() + m * n * (k // 2), scales.data_ptr() + m * n * (k // group) * 2, z,
+                                 out.data_ptr() + m * one, n, k, group, code, sm)
+            _check(rc, "moe_w4_pack")
+    return out
+
+
+def linear(x, packed, out, group: int, zeros: bool = False, bias=None, stream=None):
+    """out[b, n] = bias[n] + sum_k x[b, k] W[n, k]: x [B, K], out [B, N] (rows
+    may be strided, elements not), packed the [N, K] matrix from pack(), bias
+    [N] or None; all of one 16-bit type."""
+    lib = load_library()
+    if x.dim() != 2 or out.dim() != 2 or out.shape[0] != x.shape[0]:
+        raise ValueError(f"x {tuple(x.shape)} and out {tuple(out.shape)}: expected [B, K] and [B, N]")
+    B, K = x.shape
+    N = out.shape[1]
+    if x.stride(1) != 1 or out.stride(1) != 1:
+        raise ValueError("x and out: elements of a row must be contiguous")
+    if out.dtype != x.dtype or out.device != x.device or packed.device != x.device:
+        raise ValueError("x, packed and out: expected one device, x and out of one type")
+    if bias is not None and (bias.dtype != x.dtype or bias.numel() != N or not bias.is_contiguous()
+                             or bias.device != x.device):
+        raise ValueError(f"bias: expected {N} contiguous elements of {x.dtype} on {x.device}")
+    code = _dtype_code(x)
+    need = lib.moe_w4_packed_bytes(N, K, int(group), int(bool(zeros)))
+    if need and (packed.numel() * packed.element_size() != need or not packed.is_contiguous()):
+        raise ValueError(f"packed: {packed.numel() * packed.element_size()} bytes, expected {need} contiguous")
+    with _on(x.device):
+        sm = _stream_handle(stream) if stream is not None else _current_stream()
+        rc = lib.moe_w4_linear(x.data_ptr(), packed.data_ptr(), _ptr(bias), out.data_ptr(), B, K, N, int(group),
+                               int(bool(zeros)), x.stride(0), out.stride(0), code, sm)
+    _check(rc, "moe_w4_linear")
+    return out
