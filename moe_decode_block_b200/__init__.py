@@ -164,9 +164,25 @@ def _stream_handle(s) -> Optional[int]:
     return s.cuda_stream
 
 
-def _current_stream(device=None) -> int:
+def _current_device() -> int:
+    """Index of the current device (torch's own accessor: a call costs a
+    tenth of torch.cuda.current_device's, and the calls that use it are a few
+    microseconds long; initialises CUDA as that does)."""
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    if not torch.cuda.is_initialized():
+        return torch.cuda.current_device()
+    return torch._C._cuda_getDevice()
+
+
+def _current_stream(device: int) -> int:
+    """Handle of torch's current stream on `device`."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _packed_w4_bytes(n: int, k: int, group: int, zeros: bool) -> int:
+    """Bytes of a packed 4-bit matrix of sizes that the library accepts."""
+    return (n + 15) // 16 * (k // 64 * 512 + k // group * (64 if zeros else 32))
 
 
 def router_topk_noalloc(x, router_w, topk_ids, topk_w, top_k: int, router_bias=None, stream=None):
@@ -235,6 +251,7 @@ class MoEDecode:
         h = ctypes.c_void_p()
         _check(self._lib.moe_decode_init(ctypes.byref(self.shapes), ctypes.byref(h)), "moe_decode_init")
         self._h = h
+        self._device = _current_device()
         self._aux = None
         self._tables = {}
 
@@ -304,18 +321,26 @@ class MoEDecode:
         axis; group and zeros as the matrices were packed."""
         if batch is None:
             batch = x.shape[0]
-        H, I, Is = self.shapes.hidden, self.shapes.inter, self.shapes.shared_inter
-        for name, w, n, k in (("w13", w13, 2 * I, H), ("w2", w2, H, I), ("shared_w13", shared_w13, 2 * Is, H),
-                              ("shared_w2", shared_w2, H, Is)):
-            need = self._lib.moe_w4_packed_bytes(n, k, int(group), int(bool(zeros)))
-            one = w if not hasattr(w, "data_ptr") or name.startswith("shared") else w[0]
-            for t in (one if isinstance(one, (list, tuple)) else (one,)):
-                if hasattr(t, "data_ptr") and need and t.numel() * t.element_size() != need:
-                    raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes per matrix, expected {need}")
-        sm = _stream_handle(stream) if stream is not None else _current_stream()
-        rc = self._lib.moe_decode_forward_w4(self._h, _ptr(x), _ptr(router_w), self._table(w13), self._table(w2),
-                                             _ptr(shared_w13), _ptr(shared_w2), _ptr(out), _ptr(topk_ids),
-                                             _ptr(topk_w), int(batch), int(group), int(bool(zeros)), sm)
+        if group in (32, 64, 128):  # (another is the library's to refuse)
+            sh = self.shapes
+            H, I, Is = sh.hidden, sh.inter, sh.shared_inter
+            for name, w, n, k in (("w13", w13, 2 * I, H), ("w2", w2, H, I), ("shared_w13", shared_w13, 2 * Is, H),
+                                  ("shared_w2", shared_w2, H, Is)):
+                need = _packed_w4_bytes(n, k, group, zeros)
+                if hasattr(w, "data_ptr"):
+                    stacked = not name.startswith("shared")
+                    got = w.numel() * w.element_size()
+                    if got != need * (sh.n_experts if stacked else 1) or not w.is_contiguous():
+                        raise ValueError(f"{name}: expected {need} contiguous bytes per matrix, got {got} in all")
+                elif isinstance(w, (list, tuple)):
+                    for t in w:
+                        if hasattr(t, "data_ptr") and (t.numel() * t.element_size() != need or not t.is_contiguous()):
+                            raise ValueError(f"{name}: expected {need} contiguous bytes per matrix")
+        sm = _current_stream(self._device) if stream is None else _stream_handle(stream)
+        rc = self._lib.moe_decode_forward_w4(self._h, x.data_ptr(), router_w.data_ptr(), self._table(w13),
+                                             self._table(w2), _ptr(shared_w13), _ptr(shared_w2), out.data_ptr(),
+                                             topk_ids.data_ptr(), topk_w.data_ptr(), batch, group, 1 if zeros else 0,
+                                             sm)
         _check(rc, "moe_decode_forward_w4")
 
     def forward_host(self, x_host, router_w, w13, w2, shared_w13, shared_w2, out_host, ids_host, w_host,

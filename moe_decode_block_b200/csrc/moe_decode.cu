@@ -676,29 +676,36 @@ struct W4Pick {
   W4Kernel kern;
   int smem, ctas;  // dynamic shared memory, CTAs per SM
 };
+template <int NT, int GROUP, bool ZP, bool DOWN>
+W4Pick w4_pick_of() {
+  using C = moe::W4Cfg<NT, GROUP, ZP, moe::kW4ExpertSplit>;
+  return {moe::w4_expert_kernel<NT, GROUP, ZP, DOWN>, C::kSmem, C::kMinCtas};
+}
 template <int NT, bool DOWN>
-W4Pick pick_w4_nt(bool half_tile, bool zeros) {
-  if (half_tile && zeros) return {moe::w4_expert_kernel<NT, true, true, DOWN>, moe::W4Cfg<NT, true, true>::kSmem, moe::W4Cfg<NT, true, true>::kMinCtas};
-  if (half_tile) return {moe::w4_expert_kernel<NT, true, false, DOWN>, moe::W4Cfg<NT, true, false>::kSmem, moe::W4Cfg<NT, true, false>::kMinCtas};
-  if (zeros) return {moe::w4_expert_kernel<NT, false, true, DOWN>, moe::W4Cfg<NT, false, true>::kSmem, moe::W4Cfg<NT, false, true>::kMinCtas};
-  return {moe::w4_expert_kernel<NT, false, false, DOWN>, moe::W4Cfg<NT, false, false>::kSmem, moe::W4Cfg<NT, false, false>::kMinCtas};
+W4Pick pick_w4_nt(int group, bool zeros) {
+  switch (group) {
+    case 32: return zeros ? w4_pick_of<NT, 32, true, DOWN>() : w4_pick_of<NT, 32, false, DOWN>();
+    case 64: return zeros ? w4_pick_of<NT, 64, true, DOWN>() : w4_pick_of<NT, 64, false, DOWN>();
+    default: return zeros ? w4_pick_of<NT, 128, true, DOWN>() : w4_pick_of<NT, 128, false, DOWN>();
+  }
 }
 // The instance for the tokens that a unit can have at this batch.
 template <bool DOWN>
-W4Pick pick_w4(int batch, bool half_tile, bool zeros) {
-  if (batch <= 8) return pick_w4_nt<1, DOWN>(half_tile, zeros);
-  if (batch <= 16) return pick_w4_nt<2, DOWN>(half_tile, zeros);
-  return pick_w4_nt<4, DOWN>(half_tile, zeros);
+W4Pick pick_w4(int batch, int group, bool zeros) {
+  if (batch <= 8) return pick_w4_nt<1, DOWN>(group, zeros);
+  if (batch <= 16) return pick_w4_nt<2, DOWN>(group, zeros);
+  return pick_w4_nt<4, DOWN>(group, zeros);
 }
 
 int set_w4_attrs() {
   cudaError_t e;
   for (int batch : {8, 16, 32})
-    for (int v = 0; v < 4; ++v) {
-      const W4Pick up = pick_w4<false>(batch, v & 1, v & 2), down = pick_w4<true>(batch, v & 1, v & 2);
-      if ((e = raise_smem_limit(up.kern, up.smem)) != cudaSuccess) return fail_cuda(e);
-      if ((e = raise_smem_limit(down.kern, down.smem)) != cudaSuccess) return fail_cuda(e);
-    }
+    for (int group : {32, 64, 128})
+      for (bool zeros : {false, true}) {
+        const W4Pick up = pick_w4<false>(batch, group, zeros), down = pick_w4<true>(batch, group, zeros);
+        if ((e = raise_smem_limit(up.kern, up.smem)) != cudaSuccess) return fail_cuda(e);
+        if ((e = raise_smem_limit(down.kern, down.smem)) != cudaSuccess) return fail_cuda(e);
+      }
   return MOE_OK;
 }
 
@@ -707,7 +714,6 @@ moe::W4Geom w4_geom(int k, int group, bool zeros) {
   g.tiles = k / moe::kW4Tile;
   g.panel_bytes = (uint32_t)moe::w4_panel_bytes(k, group, zeros);
   g.entry_off = (uint32_t)(g.tiles * moe::kW4TileBytes);
-  g.group_shift = group == 128 ? 1 : 0;
   return g;
 }
 
@@ -740,12 +746,14 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
   up.plan = down.plan = h->at<Plan>(h->L.plan);
   up.shared_w = static_cast<const uint8_t*>(shared_w13);
   down.shared_w = static_cast<const uint8_t*>(shared_w2);
+  constexpr int kRowGroups = moe::kW4Warps / moe::kW4ExpertSplit;
   for (int ph = 0; ph < 2; ++ph) {
     const int I = ph ? s.inter : (s.n_shared ? s.shared_inter : 64);
     __nv_bfloat16* act = ph ? h->at<__nv_bfloat16>(h->L.a) : h->at<__nv_bfloat16>(h->L.a_s);
     moe::W4Phase& u = up.ph[ph];
     u.geom = w4_geom(s.hidden, group, zeros);
     u.blocks = 2 * I / moe::kW4Rows;
+    u.items = ceil_div(u.blocks, kRowGroups);
     u.up_off = (uint32_t)(I / 16) * u.geom.panel_bytes;
     u.x = static_cast<const __nv_bfloat16*>(x);
     u.x_cols = s.hidden;
@@ -754,6 +762,7 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
     moe::W4Phase& d = down.ph[ph];
     d.geom = w4_geom(I, group, zeros);
     d.blocks = s.hidden / moe::kW4Rows;
+    d.items = ceil_div(d.blocks, kRowGroups);
     d.x = act;
     d.x_cols = I;
     d.out = ph ? y : y_s;
@@ -763,11 +772,11 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
   const int most_units = (batch * s.top_k < s.n_experts ? batch * s.top_k : s.n_experts) +
                          batch * s.top_k / moe::kMaxUnitTokens;
   auto grid_for = [&](const moe::W4ExpertArgs& g, int ctas) {
-    const long long items = (long long)g.n_su * g.ph[0].blocks + (long long)most_units * g.ph[1].blocks;
+    const long long items = (long long)g.n_su * g.ph[0].items + (long long)most_units * g.ph[1].items;
     const long long cap = (long long)ctas * h->num_sms;
     return (int)(items < cap ? items : cap);
   };
-  const W4Pick ku = pick_w4<false>(batch, group == 32, zeros), kd = pick_w4<true>(batch, group == 32, zeros);
+  const W4Pick ku = pick_w4<false>(batch, group, zeros), kd = pick_w4<true>(batch, group, zeros);
 
   if ((e = mark(0)) != cudaSuccess) return bail(e);
   const RouterArgs ra = router_args(h, x, router_w, topk_ids, topk_w, batch);

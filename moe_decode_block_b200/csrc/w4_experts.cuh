@@ -6,7 +6,7 @@
 //   y[slot, n] = w_slot * sum_c a[slot, c] W2[c, n]
 //   out[t, n]  = bf16(x[t, n] + y[t k + 0, n] + ... + y[t k + k - 1, n] + y_shared[t, n])
 //
-// Two persistent kernels of one template: a CTA takes items (64 weight rows of
+// Two persistent kernels of one template: a CTA takes items (128 weight rows of
 // one unit -- an expert and up to 32 of its tokens), the shared expert's first:
 // those need nothing from the router, so with programmatic dependent launch
 // they stream while it runs, and the wait for its plan comes with the first
@@ -26,7 +26,8 @@ namespace moe {
 // One phase of an expert kernel: the shared expert's items, then the routed.
 struct W4Phase {
   W4Geom geom;
-  int blocks;              // items of a unit: its weight rows / 64 (UP: pairs of 32 gate and 32 up rows)
+  int blocks;              // blocks of 64 weight rows of a unit (UP: 32 gate rows and their 32 up rows)
+  int items;               // of a unit: ceil(blocks / row groups of a CTA)
   uint32_t up_off;         // UP: bytes from a gate panel to its up panel
   const __nv_bfloat16* x;  // activations [rows, x_cols]
   int x_cols;
@@ -50,77 +51,76 @@ struct W4Unit {
   int row[NT];  // activation row of the lane's token in each tile, -1: none
 };
 
-template <int NT, bool HALF, bool ZP, bool DOWN>
-__global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, HALF, ZP>::kMinCtas)
+constexpr int kW4ExpertSplit = 4;  // warps that split K; the CTA's other factor of 2 stands in the rows
+
+template <int NT, int GROUP, bool ZP, bool DOWN>
+__global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSplit>::kMinCtas)
     w4_expert_kernel(const __grid_constant__ W4ExpertArgs a, const __grid_constant__ ExpertTable tab) {
-  using C = W4Cfg<NT, HALF, ZP>;
+  using C = W4Cfg<NT, GROUP, ZP, kW4ExpertSplit>;
   using T = __nv_bfloat16;
   extern __shared__ __align__(1024) uint8_t w4_smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ks = warp % C::KS, rg = warp / C::KS;
   uint8_t* ring = w4_smem + (size_t)warp * C::kDepth * C::kSlot;
   const uint32_t ring_addr = smem_addr(ring);
   float* red = reinterpret_cast<float*>(w4_smem + (size_t)kW4Warps * C::kDepth * C::kSlot);
 
-  const int shared_items = a.n_su * a.ph[0].blocks;
+  const int shared_items = a.n_su * a.ph[0].items;
   const int step = gridDim.x;
   int n_items = shared_items;  // all items, once the plan has been read
   bool have_plan = false;
   auto read_plan = [&]() {
     if (have_plan) return;
     cudaGridDependencySynchronize();
-    n_items = shared_items + __ldcg(&a.plan->n_active) * a.ph[1].blocks;
+    n_items = shared_items + __ldcg(&a.plan->n_active) * a.ph[1].items;
     have_plan = true;
   };
   // the next grid may be put in place as this one's CTAs leave; it waits for
   // this grid's completion before it reads anything of it
   cudaTriggerProgrammaticLaunchCompletion();
-  if constexpr (DOWN) {
-    // the activations come from the grid before; weights may stream already
-  }
 
-  auto tiles_of = [&](int ph, int& t0, int& t1) {
-    const int n = a.ph[ph].geom.tiles;
-    t0 = n * warp / kW4Warps;
-    t1 = n * (warp + 1) / kW4Warps;
+  // this warp's steps of K in a phase
+  auto steps_of = [&](int ph, int& s0, int& s1) {
+    const int n = w4_steps(a.ph[ph].geom);
+    s0 = n * ks / C::KS;
+    s1 = n * (ks + 1) / C::KS;
   };
 
-  // ---- the weight stream: runs up to kDepth - 1 tiles ahead of the products
-  int p_item = blockIdx.x, p_tile = 0, p_end = 0, p_slot = 0, p_ph = 0;
-  const uint8_t* panel[kW4Panels];
-  auto p_locate = [&]() {  // panels and tile range of item p_item; false: no more
-    for (;;) {
+  // ---- the weight stream: runs up to kDepth - 1 steps ahead of the products,
+  // over the borders of items
+  int p_item = blockIdx.x, p_slot = 0;
+  W4Stream st;
+  st.valid = 0xfu;
+  auto p_locate = [&]() {  // the stream's place for item p_item; false: no more
+    for (;; p_item += step) {
       if (p_item >= shared_items) read_plan();
       if (p_item >= n_items) return false;
-      p_ph = p_item >= shared_items;
-      tiles_of(p_ph, p_tile, p_end);
-      if (p_tile < p_end) break;
-      p_item += step;  // this warp has no tile of such items
-    }
-    const W4Phase& ph = a.ph[p_ph];
-    const int i = p_item - (p_ph ? shared_items : 0);
-    const int u = i / ph.blocks, b = i - u * ph.blocks;
-    const uint8_t* w =
-        p_ph ? reinterpret_cast<const uint8_t*>(tab.p[__ldcg(&a.plan->unit_expert[u])]) : a.shared_w;
+      const int ph = p_item >= shared_items;
+      const W4Phase& P = a.ph[ph];
+      const int i = p_item - (ph ? shared_items : 0);
+      const int u = i / P.items, b = (i - u * P.items) * C::RW + rg;
+      int s0, s1;
+      steps_of(ph, s0, s1);
+      if (s0 >= s1 || b >= P.blocks) continue;  // nothing for this warp
+      const uint8_t* w = ph ? reinterpret_cast<const uint8_t*>(tab.p[__ldcg(&a.plan->unit_expert[u])]) : a.shared_w;
 #pragma unroll
-    for (int m = 0; m < kW4Panels; ++m) {
-      if constexpr (DOWN)
-        panel[m] = w + (size_t)(b * kW4Panels + m) * ph.geom.panel_bytes;
-      else
-        panel[m] = w + (size_t)(b * 2 + (m & 1)) * ph.geom.panel_bytes + (m >> 1) * (size_t)ph.up_off;
+      for (int m = 0; m < kW4Panels; ++m)
+        st.off[m] = DOWN ? m * P.geom.panel_bytes : (m & 1) * P.geom.panel_bytes + (m >> 1) * P.up_off;
+      w4_stream_start<C>(st, w + (size_t)b * (DOWN ? kW4Panels : 2) * P.geom.panel_bytes, P.geom, s0, s1, lane);
+      return true;
     }
-    return true;
   };
   bool p_more = p_locate();
   auto produce = [&]() {
     if (p_more) {
-      w4_issue<C>(ring_addr + p_slot * C::kSlot, panel, 0xfu, a.ph[p_ph].geom, p_tile, lane);
-      if (++p_tile == p_end) {
+      w4_stream_step<C, false>(st, ring_addr + p_slot, lane);
+      if (st.left <= 0) {
         p_item += step;
         p_more = p_locate();
       }
     }
     cp_async_commit();
-    p_slot = p_slot + 1 == C::kDepth ? 0 : p_slot + 1;
+    p_slot = p_slot + C::kSlot == C::kDepth * C::kSlot ? 0 : p_slot + C::kSlot;
   };
 #pragma unroll 1
   for (int d = 0; d < C::kDepth - 1; ++d) produce();
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, HALF, ZP>::kMinCtas)
     if (item >= n_items) return;
     const int ph = item >= shared_items;
     const int i = item - (ph ? shared_items : 0);
-    const int u = i / a.ph[ph].blocks;
+    const int u = i / a.ph[ph].items;
     un.begin = ph ? __ldcg(&a.plan->unit_begin[u]) : u * kMaxUnitTokens;
     un.count = ph ? __ldcg(&a.plan->unit_count[u]) : min(kMaxUnitTokens, a.batch - un.begin);
 #pragma unroll
@@ -156,71 +156,77 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, HALF, ZP>::kMinCtas)
   if constexpr (DOWN) read_plan();  // the activations are complete
   W4Unit<NT> next;
   unit_of(blockIdx.x, next);
-  uint4 xr[NT][2], xn[NT][2];
+  uint4 xa[NT][2], xb[NT][2];
   int slot = 0;
   {
     const int ph = (int)blockIdx.x >= shared_items;
-    int t0, t1;
-    tiles_of(ph, t0, t1);
+    int s0, s1;
+    steps_of(ph, s0, s1);
     const T* xp[NT];
     rows_of(next, ph, xp);
-    if (t0 < t1) w4_load_x<T, NT>(xp, t0, xn);
+    w4_load_x<T, NT>(xp, 2 * s0, s0 < s1, xa);
   }
   for (int item = blockIdx.x;; item += step) {
     if (item >= shared_items) read_plan();
     if (item >= n_items) break;
     const int ph = item >= shared_items;
+    const W4Phase& P = a.ph[ph];
     const W4Unit<NT> un = next;
     const int n_tok_tiles = (un.count + 7) >> 3;
-    int t0, t1;
-    tiles_of(ph, t0, t1);
+    const int i = item - (ph ? shared_items : 0);
+    const int b0 = i % P.items * C::RW;  // the item's first block
+    int s0, s1;
+    steps_of(ph, s0, s1);
+    if (b0 + rg >= P.blocks) s1 = s0;  // no rows for this warp
     const T* xp[NT];
     rows_of(un, ph, xp);
     unit_of(item + step, next);
     float acc[kW4Panels][NT][4] = {};
-    for (int t = t0; t < t1; ++t) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        xr[n][0] = xn[n][0];
-        xr[n][1] = xn[n][1];
-      }
-      if (t + 1 < t1) w4_load_x<T, NT>(xp, t + 1, xn);
+    float part[C::kKeep ? kW4Panels : 1][NT][4];
+    for (int s = s0; s < s1; ++s) {
+      w4_load_x<T, NT>(xp, 2 * s + 1, 2 * s + 1 < P.geom.tiles, xb);
       cp_async_wait<C::kDepth - 2>();
+    __syncwarp();  // every lane's pieces are in; every lane is done with the slot refilled next
       produce();
-      w4_tile<T, NT, HALF, ZP>(ring + slot * C::kSlot, xr, n_tok_tiles, lane, acc);
-      slot = slot + 1 == C::kDepth ? 0 : slot + 1;
+      w4_tile<T, C, 0>(ring + slot, xa, n_tok_tiles, lane, part, acc);
+      w4_load_x<T, NT>(xp, 2 * s + 2, s + 1 < s1, xa);
+      w4_tile<T, C, 1>(ring + slot, xb, n_tok_tiles, lane, part, acc);
+      slot = slot + C::kSlot == C::kDepth * C::kSlot ? 0 : slot + C::kSlot;
     }
     if (next.count > 0) {  // the next item's first activations, under this one's epilogue
       const int nph = item + step >= shared_items;
       int n0, n1;
-      tiles_of(nph, n0, n1);
+      steps_of(nph, n0, n1);
       const T* np[NT];
       rows_of(next, nph, np);
-      if (n0 < n1) w4_load_x<T, NT>(np, n0, xn);
+      w4_load_x<T, NT>(np, 2 * n0, n0 < n1, xa);
     }
     __syncthreads();  // the last item's sums have been read
-    w4_store_partials<NT>(red, warp, lane, n_tok_tiles, acc);
+    w4_store_partials<C>(red, ks, rg, lane, n_tok_tiles, acc);
     __syncthreads();
 
-    const int i = item - (ph ? shared_items : 0);
-    const int b = i % a.ph[ph].blocks;
-    const int cols = a.ph[ph].out_cols;
     if constexpr (DOWN) {
-      float* y = static_cast<float*>(a.ph[ph].out) + b * kW4Rows;
-      for (int e = tid; e < un.count * kW4Rows; e += kW4Threads) {
-        const int tok = e / kW4Rows, row = e % kW4Rows;
+      float* y = static_cast<float*>(P.out) + b0 * kW4Rows;
+      const int rows = min(C::kRows, P.out_cols - b0 * kW4Rows);
+      for (int e = tid; e < un.count * C::kRows; e += kW4Threads) {
+        const int tok = e / C::kRows, row = e % C::kRows;
+        if (row >= rows) continue;
         const float wt = ph ? __ldcg(&a.plan->assign_w[un.begin + tok]) : 1.f;
         const int r = ph ? __ldcg(&a.plan->assign_slot[un.begin + tok]) : un.begin + tok;
-        y[(size_t)r * cols + row] = wt * w4_sum_partials<NT>(red, tok, row);
+        y[(size_t)r * P.out_cols + row] = wt * w4_sum_partials<C>(red, tok, row);
       }
     } else {
-      T* o = static_cast<T*>(a.ph[ph].out) + b * (kW4Rows / 2);
-      for (int e = tid; e < un.count * (kW4Rows / 2); e += kW4Threads) {
-        const int tok = e / (kW4Rows / 2), row = e % (kW4Rows / 2);
+      // row group r: 32 gate rows, then their 32 up rows
+      T* o = static_cast<T*>(P.out) + b0 * (kW4Rows / 2);
+      const int cols = min(C::kRows / 2, P.out_cols - b0 * (kW4Rows / 2));
+      for (int e = tid; e < un.count * (C::kRows / 2); e += kW4Threads) {
+        const int tok = e / (C::kRows / 2), col = e % (C::kRows / 2);
+        if (col >= cols) continue;
         const int r = ph ? __ldcg(&a.plan->assign_slot[un.begin + tok]) : un.begin + tok;
-        const float gate = w4_sum_partials<NT>(red, tok, row);
-        const float up = w4_sum_partials<NT>(red, tok, row + kW4Rows / 2);
-        o[(size_t)r * cols + row] = __float2bfloat16_rn(silu_f32(gate) * up);
+        const int row = (col / 32) * kW4Rows + col % 32;
+        const float gate = w4_sum_partials<C>(red, tok, row);
+        const float up = w4_sum_partials<C>(red, tok, row + 32);
+        o[(size_t)r * P.out_cols + col] = __float2bfloat16_rn(silu_f32(gate) * up);
       }
     }
   }

@@ -21,15 +21,15 @@ struct W4LinearArgs {
   long long x_stride, out_stride;  // elements between tokens
 };
 
-// One CTA: kW4Rows outputs x NT * 8 tokens x its share of K; the 8 warps split
+// One CTA: 64 outputs x NT * 8 tokens x its share of K; the 8 warps split
 // that share, and the CTAs of a cluster split K between them, so a matrix with
 // few outputs still fills the GPU.  The partial sums are added in a fixed
 // order: warps first, then the cluster's CTAs through distributed shared
 // memory.  Nothing is kept in global memory between calls.
-template <typename T, int NT, bool HALF, bool ZP>
-__global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, HALF, ZP>::kMinCtas)
+template <typename T, int NT, int GROUP, bool ZP>
+__global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kMinCtas)
     w4_linear_kernel(const __grid_constant__ W4LinearArgs a) {
-  using C = W4Cfg<NT, HALF, ZP>;
+  using C = W4Cfg<NT, GROUP, ZP, kW4Warps>;
   extern __shared__ __align__(1024) uint8_t w4_smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* ring = w4_smem + (size_t)warp * C::kDepth * C::kSlot;
@@ -43,16 +43,18 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, HALF, ZP>::kMinCtas)
   const int n_tok_tiles = (n_tok + 7) / 8;
 
   const int q = rank * kW4Warps + warp, Q = S * kW4Warps;
-  const int t0 = (int)((long long)a.geom.tiles * q / Q), t1 = (int)((long long)a.geom.tiles * (q + 1) / Q);
+  const int steps = w4_steps(a.geom);
+  const int s0 = steps * q / Q, s1 = steps * (q + 1) / Q;
 
-  const uint8_t* panel[kW4Panels];
-  uint32_t valid = 0;
+  W4Stream st;
+  st.valid = 0;
+  const int p0 = row_blk * kW4Panels;
 #pragma unroll
   for (int m = 0; m < kW4Panels; ++m) {
-    const int p = row_blk * kW4Panels + m;
-    panel[m] = a.w + (size_t)(p < a.n_panels ? p : 0) * a.geom.panel_bytes;
-    valid |= p < a.n_panels ? 1u << m : 0u;
+    st.off[m] = p0 + m < a.n_panels ? m * a.geom.panel_bytes : 0u;
+    st.valid |= p0 + m < a.n_panels ? 1u << m : 0u;
   }
+  w4_stream_start<C>(st, a.w + (size_t)p0 * a.geom.panel_bytes, a.geom, s0, s1, lane);
   const T* xp[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -63,32 +65,28 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, HALF, ZP>::kMinCtas)
   const uint32_t ring_addr = smem_addr(ring);
 #pragma unroll
   for (int d = 0; d < C::kDepth - 1; ++d) {
-    if (t0 + d < t1) w4_issue<C>(ring_addr + d * C::kSlot, panel, valid, a.geom, t0 + d, lane);
+    if (s0 + d < s1) w4_stream_step<C, true>(st, ring_addr + d * C::kSlot, lane);
     cp_async_commit();
   }
   float acc[kW4Panels][NT][4] = {};
-  uint4 xr[NT][2], xn[NT][2];
-  if (t0 < t1) w4_load_x<T, NT>(xp, t0, xn);
-  int slot = 0;
-  for (int t = t0; t < t1; ++t) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      xr[n][0] = xn[n][0];
-      xr[n][1] = xn[n][1];
-    }
-    if (t + 1 < t1) w4_load_x<T, NT>(xp, t + 1, xn);
+  float part[C::kKeep ? kW4Panels : 1][NT][4];
+  uint4 xa[NT][2], xb[NT][2];
+  w4_load_x<T, NT>(xp, 2 * s0, s0 < s1, xa);
+  int slot = 0, ahead = C::kDepth - 1;
+  for (int s = s0; s < s1; ++s) {
+    w4_load_x<T, NT>(xp, 2 * s + 1, 2 * s + 1 < a.geom.tiles, xb);
     cp_async_wait<C::kDepth - 2>();
-    {
-      // the slot read in the last iteration takes the tile kDepth - 1 ahead
-      const int ahead = slot == 0 ? C::kDepth - 1 : slot - 1;
-      if (t + C::kDepth - 1 < t1)
-        w4_issue<C>(ring_addr + ahead * C::kSlot, panel, valid, a.geom, t + C::kDepth - 1, lane);
-      cp_async_commit();
-    }
-    w4_tile<T, NT, HALF, ZP>(ring + slot * C::kSlot, xr, n_tok_tiles, lane, acc);
+    __syncwarp();  // every lane's pieces are in; every lane is done with the slot refilled next
+    // the slot read in the last iteration takes the step kDepth - 1 ahead
+    if (s + C::kDepth - 1 < s1) w4_stream_step<C, true>(st, ring_addr + ahead * C::kSlot, lane);
+    cp_async_commit();
+    w4_tile<T, C, 0>(ring + slot * C::kSlot, xa, n_tok_tiles, lane, part, acc);
+    w4_load_x<T, NT>(xp, 2 * s + 2, s + 1 < s1, xa);
+    w4_tile<T, C, 1>(ring + slot * C::kSlot, xb, n_tok_tiles, lane, part, acc);
+    ahead = slot;
     slot = slot + 1 == C::kDepth ? 0 : slot + 1;
   }
-  w4_store_partials<NT>(red, warp, lane, n_tok_tiles, acc);
+  w4_store_partials<C>(red, warp, 0, lane, n_tok_tiles, acc);
   __syncthreads();
 
   const int row0 = row_blk * kW4Rows;
@@ -101,7 +99,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, HALF, ZP>::kMinCtas)
   if (S == 1) {
     for (int i = tid; i < n_tok * kW4Rows; i += kW4Threads) {
       const int tok = i / kW4Rows, row = i % kW4Rows;
-      store(tok, row, w4_sum_partials<NT>(red, tok, row));
+      store(tok, row, w4_sum_partials<C>(red, tok, row));
     }
     return;
   }
@@ -109,14 +107,14 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, HALF, ZP>::kMinCtas)
   // by one thread), then every CTA of the cluster adds a share of them
   for (int i = tid; i < n_tok * kW4Rows; i += kW4Threads) {
     const int tok = i / kW4Rows, row = i % kW4Rows;
-    const float v = w4_sum_partials<NT>(red, tok, row);
-    red[tok * kW4RedPitch + row] = v;
+    const float v = w4_sum_partials<C>(red, tok, row);
+    red[tok * C::kPitch + row] = v;
   }
   cluster.sync();
   for (int i = rank * kW4Threads + tid; i < n_tok * kW4Rows; i += S * kW4Threads) {
     const int tok = i / kW4Rows, row = i % kW4Rows;
     float v = 0.f;
-    for (int r = 0; r < S; ++r) v += cluster.map_shared_rank(red, r)[tok * kW4RedPitch + row];
+    for (int r = 0; r < S; ++r) v += cluster.map_shared_rank(red, r)[tok * C::kPitch + row];
     store(tok, row, v);
   }
   cluster.sync();  // no CTA leaves while another reads its sums
@@ -167,39 +165,42 @@ bool w4_shape_ok(int n_out, int k, int group) {
 bool dtype_ok(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP16; }
 
 // Cluster size (CTAs that split K): as many as fill two CTAs on every SM, as
-// long as every warp keeps two tiles of its own.
-int cluster_for(int row_blocks, int tiles, int slots) {
+// long as every warp keeps a step of its own.
+int cluster_for(int row_blocks, int steps, int slots) {
   int s = 1;
-  while (s < 8 && 2 * s * row_blocks <= slots && tiles >= 2 * s * kW4Warps * 2) s *= 2;
+  while (s < 8 && 2 * s * row_blocks <= slots && steps >= 2 * s * kW4Warps) s *= 2;
   return s;
 }
 
-template <typename T, int NT, bool HALF, bool ZP>
+template <typename T, int NT, int GROUP, bool ZP>
 int launch_linear(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) {
-  using C = W4Cfg<NT, HALF, ZP>;
+  using C = W4Cfg<NT, GROUP, ZP, kW4Warps>;
   static std::atomic<uint64_t> raised{0};
-  const auto kern = w4_linear_kernel<T, NT, HALF, ZP>;
+  const auto kern = w4_linear_kernel<T, NT, GROUP, ZP>;
   const int rc = host_raise_smem(kern, C::kSmem, dev, raised);
   if (rc != MOE_OK) return rc;
   const int row_blocks = (a.n_panels + kW4Panels - 1) / kW4Panels;
   const int tok_blocks = (a.batch + NT * 8 - 1) / (NT * 8);
-  const int s = cluster_for(row_blocks * tok_blocks, a.geom.tiles, C::kMinCtas * num_sms);
+  const int s = cluster_for(row_blocks * tok_blocks, w4_steps(a.geom), C::kMinCtas * num_sms);
   const cudaError_t e =
       host_launch(kern, dim3((unsigned)(row_blocks * s), (unsigned)tok_blocks), kW4Threads, C::kSmem, st, s, false, a);
   return e == cudaSuccess ? MOE_OK : host_fail_cuda(e);
 }
 
-template <typename T, bool HALF, bool ZP>
+template <typename T, int GROUP, bool ZP>
 int pick_nt(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) {
-  if (a.batch <= 8) return launch_linear<T, 1, HALF, ZP>(a, dev, num_sms, st);
-  if (a.batch <= 16) return launch_linear<T, 2, HALF, ZP>(a, dev, num_sms, st);
-  return launch_linear<T, 4, HALF, ZP>(a, dev, num_sms, st);
+  if (a.batch <= 8) return launch_linear<T, 1, GROUP, ZP>(a, dev, num_sms, st);
+  if (a.batch <= 16) return launch_linear<T, 2, GROUP, ZP>(a, dev, num_sms, st);
+  return launch_linear<T, 4, GROUP, ZP>(a, dev, num_sms, st);
 }
 
 template <typename T>
-int pick_linear(const W4LinearArgs& a, bool half_tile, bool zeros, int dev, int num_sms, cudaStream_t st) {
-  if (half_tile) return zeros ? pick_nt<T, true, true>(a, dev, num_sms, st) : pick_nt<T, true, false>(a, dev, num_sms, st);
-  return zeros ? pick_nt<T, false, true>(a, dev, num_sms, st) : pick_nt<T, false, false>(a, dev, num_sms, st);
+int pick_linear(const W4LinearArgs& a, int group, bool zeros, int dev, int num_sms, cudaStream_t st) {
+  switch (group) {
+    case 32: return zeros ? pick_nt<T, 32, true>(a, dev, num_sms, st) : pick_nt<T, 32, false>(a, dev, num_sms, st);
+    case 64: return zeros ? pick_nt<T, 64, true>(a, dev, num_sms, st) : pick_nt<T, 64, false>(a, dev, num_sms, st);
+    default: return zeros ? pick_nt<T, 128, true>(a, dev, num_sms, st) : pick_nt<T, 128, false>(a, dev, num_sms, st);
+  }
 }
 
 }  // namespace
@@ -261,12 +262,11 @@ int moe_w4_linear(const void* x, const void* packed, const void* bias, void* out
   a.geom.tiles = in_features / kW4Tile;
   a.geom.panel_bytes = (uint32_t)w4_panel_bytes(in_features, group, has_zeros != 0);
   a.geom.entry_off = (uint32_t)(a.geom.tiles * kW4TileBytes);
-  a.geom.group_shift = group == 128 ? 1 : 0;
   a.x_stride = x_stride;
   a.out_stride = out_stride;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == MOE_DTYPE_BF16 ? pick_linear<__nv_bfloat16>(a, group == 32, has_zeros != 0, dev, sms, st)
-                                 : pick_linear<__half>(a, group == 32, has_zeros != 0, dev, sms, st);
+  return dtype == MOE_DTYPE_BF16 ? pick_linear<__nv_bfloat16>(a, group, has_zeros != 0, dev, sms, st)
+                                 : pick_linear<__half>(a, group, has_zeros != 0, dev, sms, st);
 }
 
 }  // extern "C"

@@ -10,20 +10,27 @@ and its forward_w4.
 from __future__ import annotations
 
 from contextlib import nullcontext
-from typing import Optional
 
-from . import MOE_DTYPE_BF16, MOE_DTYPE_FP16, _check, _current_stream, _ptr, _stream_handle, load_library
+from . import (MOE_DTYPE_BF16, MOE_DTYPE_FP16, _check, _current_device, _current_stream, _stream_handle,
+               load_library)
 
 MAX_BATCH = 64
+_CODES = {}
+
+
+def _codes() -> dict:
+    """torch dtype -> MOE_DTYPE_* of the products."""
+    if not _CODES:
+        import torch
+        _CODES.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16})
+    return _CODES
 
 
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype is torch.bfloat16:
-        return MOE_DTYPE_BF16
-    if t.dtype is torch.float16:
-        return MOE_DTYPE_FP16
-    raise ValueError(f"expected bfloat16 or float16, got {t.dtype}")
+    code = _codes().get(t.dtype)
+    if code is None:
+        raise ValueError(f"expected bfloat16 or float16, got {t.dtype}")
+    return code
 
 
 def _on(device):
@@ -32,7 +39,7 @@ def _on(device):
     import torch
     if device.type != "cuda":
         raise ValueError(f"expected tensors on a GPU, got {device}")
-    return nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return nullcontext() if device.index == _current_device() else torch.cuda.device(device)
 
 
 def packed_bytes(out_features: int, in_features: int, group: int, zeros: bool = False) -> int:
@@ -70,7 +77,7 @@ def pack(codes, scales, zeros=None, out=None, stream=None):
     elif out.shape != shape or out.dtype is not torch.uint8 or not out.is_contiguous() or out.device != codes.device:
         raise ValueError(f"out: expected a contiguous uint8 {shape} tensor on {codes.device}")
     with _on(codes.device):
-        sm = _stream_handle(stream) if stream is not None else _current_stream()
+        sm = _stream_handle(stream) if stream is not None else _current_stream(codes.get_device())
         for m in range(codes[..., 0, 0].numel()):
             z = None if zeros is None else zeros.data_ptr() + m * n * (k // group)
             rc = lib.moe_w4_pack(codes.data_ptr() + m * n * (k // 2), scales.data_ptr() + m * n * (k // group) * 2, z,
@@ -79,29 +86,50 @@ def pack(codes, scales, zeros=None, out=None, stream=None):
     return out
 
 
+def _refuse_linear(x, packed, out, group, zeros, bias):
+    """Say what is wrong with linear()'s arguments."""
+    if x.dim() != 2 or out.dim() != 2 or out.shape[0] != x.shape[0]:
+        raise ValueError(f"x {tuple(x.shape)} and out {tuple(out.shape)}: expected [B, K] and [B, N]")
+    _dtype_code(x)
+    for name, t in (("x", x), ("packed", packed), ("out", out), ("bias", bias)):
+        if t is not None and (t.device.type != "cuda" or t.device != x.device):
+            raise ValueError(f"{name}: on {t.device}, expected one GPU (x is on {x.device})")
+    if out.dtype != x.dtype:
+        raise ValueError(f"out: {out.dtype}, x is {x.dtype}")
+    if x.stride(1) != 1 or out.stride(1) != 1:
+        raise ValueError("x and out: elements of a row must be contiguous")
+    N = out.shape[1]
+    if bias is not None and (bias.dtype != x.dtype or bias.numel() != N or not bias.is_contiguous()):
+        raise ValueError(f"bias: expected {N} contiguous elements of {x.dtype}")
+    raise ValueError(f"packed: expected {packed_bytes(N, x.shape[1], group, zeros)} contiguous bytes (uint8), got "
+                     f"{packed.numel()} of {packed.dtype}")
+
+
 def linear(x, packed, out, group: int, zeros: bool = False, bias=None, stream=None):
     """out[b, n] = bias[n] + sum_k x[b, k] W[n, k]: x [B, K], out [B, N] (rows
     may be strided, elements not), packed the [N, K] matrix from pack(), bias
-    [N] or None; all of one 16-bit type."""
-    lib = load_library()
-    if x.dim() != 2 or out.dim() != 2 or out.shape[0] != x.shape[0]:
-        raise ValueError(f"x {tuple(x.shape)} and out {tuple(out.shape)}: expected [B, K] and [B, N]")
+    [N] or None; all of one 16-bit type.  `stream` belongs to x's device."""
     B, K = x.shape
-    N = out.shape[1]
-    if x.stride(1) != 1 or out.stride(1) != 1:
-        raise ValueError("x and out: elements of a row must be contiguous")
-    if out.dtype != x.dtype or out.device != x.device or packed.device != x.device:
-        raise ValueError("x, packed and out: expected one device, x and out of one type")
-    if bias is not None and (bias.dtype != x.dtype or bias.numel() != N or not bias.is_contiguous()
-                             or bias.device != x.device):
-        raise ValueError(f"bias: expected {N} contiguous elements of {x.dtype} on {x.device}")
-    code = _dtype_code(x)
-    need = lib.moe_w4_packed_bytes(N, K, int(group), int(bool(zeros)))
-    if need and (packed.numel() * packed.element_size() != need or not packed.is_contiguous()):
-        raise ValueError(f"packed: {packed.numel() * packed.element_size()} bytes, expected {need} contiguous")
-    with _on(x.device):
-        sm = _stream_handle(stream) if stream is not None else _current_stream()
-        rc = lib.moe_w4_linear(x.data_ptr(), packed.data_ptr(), _ptr(bias), out.data_ptr(), B, K, N, int(group),
-                               int(bool(zeros)), x.stride(0), out.stride(0), code, sm)
-    _check(rc, "moe_w4_linear")
+    Bo, N = out.shape
+    sx, so = x.stride(), out.stride()
+    dtype, dev = x.dtype, x.get_device()
+    code = _codes().get(dtype)
+    # a packed matrix's size; a shape that the library refuses is its to refuse
+    need = (N + 15) // 16 * (K // 64 * 512 + (K // group * (64 if zeros else 32) if group > 0 else 0))
+    if (code is None or dev < 0 or Bo != B or sx[1] != 1 or so[1] != 1 or out.dtype is not dtype
+            or out.get_device() != dev or packed.get_device() != dev or packed.numel() != need
+            or packed.element_size() != 1 or not packed.is_contiguous()
+            or (bias is not None and (bias.dtype is not dtype or bias.numel() != N or bias.get_device() != dev
+                                      or not bias.is_contiguous()))):
+        _refuse_linear(x, packed, out, group, zeros, bias)
+    call = load_library().moe_w4_linear
+    args = (x.data_ptr(), packed.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), B, K, N, group,
+            1 if zeros else 0, sx[0], so[0], code)
+    if dev == _current_device():
+        rc = call(*args, _current_stream(dev) if stream is None else _stream_handle(stream))
+    else:
+        with _on(x.device):
+            rc = call(*args, _current_stream(dev) if stream is None else _stream_handle(stream))
+    if rc:
+        _check(rc, "moe_w4_linear")
     return out
