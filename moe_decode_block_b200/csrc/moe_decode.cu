@@ -746,6 +746,7 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
   up.plan = down.plan = h->at<Plan>(h->L.plan);
   up.shared_w = static_cast<const uint8_t*>(shared_w13);
   down.shared_w = static_cast<const uint8_t*>(shared_w2);
+  auto inverse = [](int d) { return d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0u; };
   constexpr int kRowGroups = moe::kW4Warps / moe::kW4ExpertSplit;
   for (int ph = 0; ph < 2; ++ph) {
     const int I = ph ? s.inter : (s.n_shared ? s.shared_inter : 64);
@@ -754,6 +755,7 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
     u.geom = w4_geom(s.hidden, group, zeros);
     u.blocks = 2 * I / moe::kW4Rows;
     u.items = ceil_div(u.blocks, kRowGroups);
+    u.items_inv = inverse(u.items);
     u.up_off = (uint32_t)(I / 16) * u.geom.panel_bytes;
     u.x = static_cast<const __nv_bfloat16*>(x);
     u.x_cols = s.hidden;
@@ -763,6 +765,7 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
     d.geom = w4_geom(I, group, zeros);
     d.blocks = s.hidden / moe::kW4Rows;
     d.items = ceil_div(d.blocks, kRowGroups);
+    d.items_inv = inverse(d.items);
     d.x = act;
     d.x_cols = I;
     d.out = ph ? y : y_s;

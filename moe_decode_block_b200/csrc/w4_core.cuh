@@ -6,11 +6,19 @@
 //
 // q in 0..15, z = 8 without zero points, G = 32, 64 or 128 inputs to a group.
 //
-// Mathematics.  Within a 64-input tile (32 inputs for G = 32) the scale is one
-// number per output, so the tile's sum over (q - z) * x is taken by mma.sync
-// with fp32 accumulators -- q - z is a small whole number, exact in bf16 and
-// fp16, and so is its product's operand x -- and the fp32 result is multiplied
-// by the scale once: no weight is ever rounded.
+// Mathematics.  Within a group the scale and the zero point are one number per
+// output, so the group's sum of q x is taken by mma.sync with fp32 accumulators,
+// the sum of x beside it, and s (sum q x - z sum x) added in fp32: no weight is
+// ever rounded.  The codes go to the tensor core as they are: a 16-bit float
+// with nothing but a code in its lowest bits is q times the type's smallest
+// subnormal, and in bits 4..7 it is 16 q times that -- also where bit 7 is
+// bf16's lowest exponent bit, since the first binade of normal numbers continues
+// the subnormals' steps.  mma.sync takes subnormal operands exactly (measured).
+// So an operand register costs one mask, and every second one no shift.  The
+// powers of two come off in the end; bf16 activations are multiplied by 2^64 on
+// their way in (exact) so that their products with 2^-133 stay normal fp32
+// numbers: |x| is held from 2^-57 to 2^63.  An infinite activation gives NaN
+// (infinity minus infinity), as do sums beyond fp32.
 //
 // Layout (moe_w4_pack).  A matrix is stored as panels of 16 outputs; a panel is
 // its K / 64 tiles of 512 bytes, then its group entries.  A tile is in
@@ -19,17 +27,19 @@
 // panel is one contiguous stream.  Word s of a lane holds step s of the tile:
 // bits 4j / 16 + 4j are output g + 8 (j & 1), inputs
 // 32 (s >> 1) + 8 t + 4 (s & 1) + 2 (j >> 1) and the next -- the order that
-// turns into the four A registers of m16n8k16 with one mask and one exact
-// subtraction each, while the lane's B registers are 16 contiguous bytes of x.
+// turns into the four A registers of m16n8k16 by masks, while the lane's B registers are 16 contiguous bytes of x.
 //
-// What bounds it.  Up to 16 tokens: HBM for large matrices, and close behind it
-// the instructions that turn codes into operands (11 per 8 codes in bf16, 9 in
-// fp16; at 46 weights a clock and SM, the rate of HBM, that is two thirds of
-// the ALU pipe).  So everything else is kept off the issue slots: a step of a
-// warp is a pair of tiles (128 inputs) of 4 panels, addresses advance by
-// constants, x is read as whole 16-byte B fragments straight from L1 / L2.
-// Weights come through a warp's own ring of asynchronous 16-byte copies: no
-// barrier between warps, and no wait that another thread would have to end.
+// What bounds it.  HBM for large matrices up to 16 tokens, and not far behind it
+// the ALU pipe: 5 of its instructions for 8 codes, two cycles each, are 40 of
+// the 88 cycles that a scheduler has for 1,024 weights at HBM's rate (46 weights
+// a clock and SM).  (Subtracting the zero point from every operand, with its
+// shifts, took 28 ALU and 16 more instructions for 1,024 codes instead of 20,
+// and held the kernel to 40 weights a clock.)  So everything else is kept off
+// the issue slots: a step of a warp is a pair of tiles (128 inputs) of 4 panels,
+// addresses advance by constants, x is read as whole 16-byte B fragments
+// straight from L1 / L2.  Weights come through a warp's own ring of asynchronous
+// 16-byte copies: no barrier between warps, and no wait that another thread
+// would have to end.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -47,6 +57,7 @@ constexpr int kW4Warps = 8;        // warps of a CTA
 constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Panels = 4;       // panels (of 16 outputs) of a warp's accumulators
 constexpr int kW4Rows = 16 * kW4Panels;
+constexpr int kW4SumPitch = kW4Rows + 4;  // 2 * pitch = 8 mod 32: conflict-free fragment stores
 
 // Bytes of one group entry of a panel: 16 scales, with zero points 16 of those too.
 __host__ __device__ constexpr int w4_entry_bytes(bool zeros) { return zeros ? 64 : 32; }
@@ -66,25 +77,27 @@ struct W4Cfg {
   static constexpr bool ZP = ZP_;
   static constexpr int RW = kW4Warps / KS;              // row groups of 64 outputs
   static constexpr int kRows = RW * kW4Rows;            // outputs of a CTA
-  static constexpr int kPitch = kRows + 4;              // 2 * pitch = 8 mod 32: conflict-free fragment stores
   static constexpr int kLaneEntry = ZP ? 8 : 4;         // a lane's bytes of an entry: outputs g and g + 8
   static constexpr int kEntries = 2 * kW4Tile / GROUP;  // entries of a step (a pair of tiles)
   static constexpr int kEntryBytes = 8 * kLaneEntry;    // of one entry: 16 outputs
   static constexpr int kChunks = kEntries * kEntryBytes / 16;  // 16-byte pieces of a panel's entries of a step
-  // groups of 128 keep their sums over both tiles of a step before the scale;
-  // with more token tiles those sums would cost too many registers
-  static constexpr bool kKeep = kEntries == 1 && NT == 1;
+  static constexpr int kPieces = kChunks * kW4Panels;          // of 4 panels': up to two for each lane
   static constexpr int kCodes = 2 * kW4Panels * kW4TileBytes;
-  static constexpr int kSlot = kCodes + kW4Panels * kEntries * kEntryBytes;  // a warp's ring slot
-  static constexpr int kRed = KS * NT * 8 * kPitch * 4;
+  static constexpr int kSlot = kCodes + kPieces * 16;       // a warp's ring slot: a step of 4 panels
+  // A warp's sums of an item, [token][row], beside the ring.  (In the ring slot
+  // just emptied they would leave room for a third step, but hold up the refill
+  // until the CTA has added them: 303 against 285 us for a full-size block of 8
+  // tokens.)
+  static constexpr int kSums = NT * 8 * kW4SumPitch * 4;
   // two CTAs on an SM up to 16 tokens where two rings of two steps fit, one
   // above (more accumulators)
-  static constexpr int fit(int kb) { return (kb * 1024 - 1024 - kRed) / (kW4Warps * kSlot); }
-  static constexpr int kMinCtas = NT <= 2 && fit(113) >= 2 ? 2 : 1;
-  static constexpr int kFit = fit(kMinCtas == 2 ? 113 : 226);
+  static constexpr int fit(int kb) { return (kb * 1024 - 2048 - kW4Warps * kSums) / (kW4Warps * kSlot); }
+  static constexpr int kMinCtas = NT <= 2 && fit(114) >= 2 ? 2 : 1;
+  static constexpr int kFit = fit(kMinCtas == 2 ? 114 : 227);
   static constexpr int kDepth = kFit > 4 ? 4 : kFit;
-  static constexpr int kSmem = kW4Warps * kDepth * kSlot + kRed;
-  static_assert(kDepth >= 2, "ring depth");
+  static constexpr int kRing = kW4Warps * kDepth * kSlot;
+  static constexpr int kSmem = kRing + kW4Warps * kSums;
+  static_assert(kDepth >= 2 && kPieces <= 64, "ring");
 };
 
 // Geometry of a packed matrix, the same for every expert of a launch.
@@ -101,52 +114,39 @@ __host__ __device__ inline int w4_steps(const W4Geom& g) { return (g.tiles + 1) 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
-  uint32_t r;  // (a & mask) | bits in one instruction
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
-  return r;
+// A word's codes as the A operands of one mma step: outputs g (bits 0..3 of the
+// 16-bit halves) and g + 8 (bits 4..7).
+__device__ __forceinline__ void w4_operands(uint32_t w, uint32_t (&a)[4]) {
+  const uint32_t w8 = w >> 8;
+  a[0] = w & 0x000f000fu;
+  a[1] = w & 0x00f000f0u;
+  a[2] = w8 & 0x000f000fu;
+  a[3] = w8 & 0x00f000f0u;
 }
 
-// Per type: codes to A operands, the zero-point constants, scales, the mma.
+// Per type: the mma, scales, and the powers of two.
 template <typename T>
 struct W4Type;
 
 template <>
 struct W4Type<__nv_bfloat16> {
-  // 0x4300 | v is 128 + v; subtracting 128 + z is exact.
-  static __device__ __forceinline__ uint32_t splat(float v) {
-    const __nv_bfloat162 h = __float2bfloat162_rn(v);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+  static constexpr float kUnit = 0x1p+69f;  // 2^133 (a code's unit) / 2^64 (of x)
+  static __device__ __forceinline__ uint32_t scale_x(uint32_t v) {
+    const uint32_t k = 0x5f805f80u;  // 2^64
     const __nv_bfloat162 r =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&k));
     return *reinterpret_cast<const uint32_t*>(&r);
   }
-  static __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r =
-        __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  // what is subtracted from the words of outputs g and g + 8
-  static __device__ __forceinline__ void zero_consts(uint32_t zp, uint32_t& zg, uint32_t& zg8) {
-    const uint32_t base = splat(128.f);
-    zg = add(base, __byte_perm(zp, zp, 0x1010));
-    zg8 = add(base, __byte_perm(zp, zp, 0x3232));
-  }
-  static __device__ __forceinline__ void dequant(uint32_t w, uint32_t zg, uint32_t zg8, uint32_t (&a)[4]) {
-    a[0] = sub(and_or(w, 0x000f000fu, 0x43004300u), zg);
-    a[1] = sub(and_or(w >> 4, 0x000f000fu, 0x43004300u), zg8);
-    a[2] = sub(and_or(w >> 8, 0x000f000fu, 0x43004300u), zg);
-    a[3] = sub(and_or(w >> 12, 0x000f000fu, 0x43004300u), zg8);
-  }
-  static __device__ __forceinline__ void scales(uint32_t s, float& s0, float& s1) { bf16x2_to_f32(s, s0, s1); }
+  static __device__ __forceinline__ void pair_f32(uint32_t s, float& s0, float& s1) { bf16x2_to_f32(s, s0, s1); }
   // c += a b; FIRST: c = a b
   template <bool FIRST>
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -162,34 +162,9 @@ struct W4Type<__nv_bfloat16> {
 
 template <>
 struct W4Type<__half> {
-  static __device__ __forceinline__ uint32_t splat(float v) {
-    const __half2 h = __float2half2_rn(v);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
-                              *reinterpret_cast<const __half2*>(&c));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  // 0x6400 | v is 1024 + v and 0x6400 | 16 v is 1024 + 16 v: outputs g take
-  // (1024 + v) - (1024 + z), outputs g + 8 (1024 + 16 v) / 16 - (64 + z), both
-  // exact and the second without a shift.
-  static __device__ __forceinline__ void zero_consts(uint32_t zp, uint32_t& zg, uint32_t& zg8) {
-    zg = sub(__byte_perm(zp, zp, 0x1010), splat(-1024.f));
-    zg8 = sub(splat(-64.f), __byte_perm(zp, zp, 0x3232));
-  }
-  static __device__ __forceinline__ void dequant(uint32_t w, uint32_t zg, uint32_t zg8, uint32_t (&a)[4]) {
-    const uint32_t w8 = w >> 8, sixteenth = 0x2c002c00u;
-    a[0] = sub(and_or(w, 0x000f000fu, 0x64006400u), zg);
-    a[1] = fma(and_or(w, 0x00f000f0u, 0x64006400u), sixteenth, zg8);
-    a[2] = sub(and_or(w8, 0x000f000fu, 0x64006400u), zg);
-    a[3] = fma(and_or(w8, 0x00f000f0u, 0x64006400u), sixteenth, zg8);
-  }
-  static __device__ __forceinline__ void scales(uint32_t s, float& s0, float& s1) {
+  static constexpr float kUnit = 0x1p+24f;
+  static __device__ __forceinline__ uint32_t scale_x(uint32_t v) { return v; }
+  static __device__ __forceinline__ void pair_f32(uint32_t s, float& s0, float& s1) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s));
     s0 = f.x;
     s1 = f.y;
@@ -217,6 +192,7 @@ struct W4Stream {
   uint32_t valid;           // bit m: panel m exists (otherwise it reads as zero)
 };
 
+// At steps [step0, step1) of K.
 template <typename C>
 __device__ __forceinline__ void w4_stream_start(W4Stream& st, const uint8_t* panel0, const W4Geom& g, int step0,
                                                 int step1, int lane) {
@@ -226,7 +202,7 @@ __device__ __forceinline__ void w4_stream_start(W4Stream& st, const uint8_t* pan
 #pragma unroll
   for (int i = 1; i < kW4Panels; ++i) off = m == i ? st.off[i] : off;
   st.entry = panel0 + off + g.entry_off + (size_t)step0 * (C::kEntries * C::kEntryBytes) + lane % C::kChunks * 16;
-  if constexpr (C::kChunks * kW4Panels > 32) st.entry2 = (m == 0 ? st.off[2] : st.off[3]) - off;
+  if constexpr (C::kPieces > 32) st.entry2 = (m == 0 ? st.off[2] : st.off[3]) - off;
   st.left = min(g.tiles, 2 * step1) - 2 * step0;
 }
 
@@ -234,135 +210,243 @@ __device__ __forceinline__ void w4_stream_start(W4Stream& st, const uint8_t* pan
 // may be missing.
 template <typename C, bool CHECK>
 __device__ __forceinline__ void w4_stream_step(W4Stream& st, uint32_t slot, int lane) {
-  const bool second = st.left > 1;
   const uint32_t dst = slot + lane * 16;
+  if (!CHECK && st.left > 1) {
 #pragma unroll
-  for (int m = 0; m < kW4Panels; ++m) {
-    const bool v = !CHECK || ((st.valid >> m) & 1u);
-    const uint8_t* p = st.code + st.off[m];
-    cp_async_16(dst + 2 * m * kW4TileBytes, p, v);
-    cp_async_16(dst + (2 * m + 1) * kW4TileBytes, second ? p + kW4TileBytes : p, v && second);
-  }
-  // (groups of 128 come with K in whole pairs; the other groups' entries of a
-  // missing tile, the second half of a panel's pieces, are not read)
-  constexpr int kPieces = C::kChunks * kW4Panels;
-  const bool in = C::kEntries == 1 || second || lane % C::kChunks < C::kChunks / 2;
-  const int m = lane / C::kChunks;
-  if (kPieces >= 32 || lane < kPieces) {
-    cp_async_16(dst + C::kCodes, in ? st.entry : st.code, in && (!CHECK || ((st.valid >> m) & 1u)));
-    if constexpr (kPieces > 32)
-      cp_async_16(dst + C::kCodes + 512, in ? st.entry + st.entry2 : st.code,
-                   in && (!CHECK || ((st.valid >> (m + 2)) & 1u)));
+    for (int m = 0; m < kW4Panels; ++m) {
+      const uint8_t* p = st.code + st.off[m];
+      cp_async_16(dst + 2 * m * kW4TileBytes, p);
+      cp_async_16(dst + (2 * m + 1) * kW4TileBytes, p + kW4TileBytes);
+    }
+    if (C::kPieces >= 32 || lane < C::kPieces) {
+      cp_async_16(dst + C::kCodes, st.entry);
+      if constexpr (C::kPieces > 32) cp_async_16(dst + C::kCodes + 512, st.entry + st.entry2);
+    }
+  } else {
+    // a missing panel is zero (its outputs are not stored), a missing tile is
+    // not copied (and not multiplied); groups of 128 come with K in whole
+    // pairs, the other groups' entries of a missing tile -- the second half of
+    // a panel's pieces -- do not exist
+    const bool second = st.left > 1;
+#pragma unroll
+    for (int m = 0; m < kW4Panels; ++m) {
+      const bool v = !CHECK || ((st.valid >> m) & 1u);
+      const uint8_t* p = st.code + st.off[m];
+      cp_async_16(dst + 2 * m * kW4TileBytes, p, v);
+      if (second) cp_async_16(dst + (2 * m + 1) * kW4TileBytes, p + kW4TileBytes, v);
+    }
+    const bool in = C::kEntries == 1 || second || lane % C::kChunks < C::kChunks / 2;
+    const int m = lane / C::kChunks;
+    if (C::kPieces >= 32 || lane < C::kPieces) {
+      cp_async_16(dst + C::kCodes, in ? st.entry : st.code, in && (!CHECK || ((st.valid >> m) & 1u)));
+      if constexpr (C::kPieces > 32)
+        cp_async_16(dst + C::kCodes + 512, in ? st.entry + st.entry2 : st.code,
+                    in && (!CHECK || ((st.valid >> (m + 2)) & 1u)));
+    }
   }
   st.code += 2 * kW4TileBytes;
   st.entry += C::kEntries * C::kEntryBytes;
   st.left -= 2;
 }
 
-// Tile `half` of the step in `slot` times the lane's x (2 x 16 bytes per token
-// tile) into acc.  With kKeep the sums stay in `part` from the first half to the
-// second.  n_tok_tiles <= NT is the same for the whole warp.
-template <typename T, typename C, int HALF>
-__device__ __forceinline__ void w4_tile(const uint8_t* slot, const uint4 (&xr)[C::NT][2], int n_tok_tiles, int lane,
-                                        float (&part)[C::kKeep ? kW4Panels : 1][C::NT][4],
-                                        float (&acc)[kW4Panels][C::NT][4]) {
+// FIRST .. FIRST + COUNT of a step's two tiles (in `slot`) times the lane's x (2
+// x 16 bytes per tile and token tile) into acc, in units of 1 / kUnit (outputs g
+// + 8: 16 / kUnit).  A group's sum is scaled once; groups of 128 are cut between
+// the tiles where these are taken one by one.  N <= NT: token tiles that exist.
+template <typename T, typename C, int N, int FIRST, int COUNT>
+__device__ __forceinline__ void w4_tiles(const uint8_t* slot, const uint4 (&xv)[COUNT][C::NT][2], int lane,
+                                         float (&acc)[kW4Panels][C::NT][4]) {
   using W = W4Type<T>;
-  constexpr int NT = C::NT;
-  constexpr int kPer = C::kEntries == 4 ? 2 : 4;  // mma steps of a group inside this tile
+  constexpr int kGroups = C::kEntries * COUNT / 2 > 0 ? C::kEntries * COUNT / 2 : 1;
+  constexpr int kPer = 4 * COUNT / kGroups;  // mma steps of a group
+  // B operands, and the groups' z0 sum x: z0 = 8, or 1 where zero points come
+  // with the entries
+  uint32_t xr[4 * COUNT][N][2];
+  float sum[kGroups][N][2];
+  const uint32_t one = C::ZP ? 0x00010001u : 0x00080008u, ones[4] = {one, one, one, one};
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+#pragma unroll
+    for (int s = 0; s < 4 * COUNT; ++s) {
+      const uint4 v = xv[s / 4][n][(s >> 1) & 1];
+      xr[s][n][0] = W::scale_x((s & 1) ? v.z : v.x);
+      xr[s][n][1] = W::scale_x((s & 1) ? v.w : v.y);
+    }
+#pragma unroll
+    for (int e = 0; e < kGroups; ++e) {
+      float c[4];
+      W::template mma<true>(c, ones, xr[e * kPer][n][0], xr[e * kPer][n][1]);
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) W::template mma<false>(c, ones, xr[e * kPer + i][n][0], xr[e * kPer + i][n][1]);
+      sum[e][n][0] = c[0];
+      sum[e][n][1] = c[1];
+    }
+  }
 #pragma unroll
   for (int m = 0; m < kW4Panels; ++m) {
-    const uint4 wv = *reinterpret_cast<const uint4*>(slot + (2 * m + HALF) * kW4TileBytes + lane * 16);
-    const uint32_t words[4] = {wv.x, wv.y, wv.z, wv.w};
-    float(&pt)[NT][4] = part[C::kKeep ? m : 0];
+    uint32_t words[4 * COUNT];
 #pragma unroll
-    for (int e = 0; e < 4 / kPer; ++e) {
-      constexpr int kHalfEntries = C::kEntries / 2;  // entries of a tile, 0 for groups of 128
-      const int ei = C::kEntries == 1 ? 0 : HALF * kHalfEntries + e;
-      const uint8_t* ent = slot + C::kCodes + (m * C::kEntries + ei) * C::kEntryBytes + (lane >> 2) * C::kLaneEntry;
-      uint32_t sc, zg, zg8;
+    for (int i = 0; i < COUNT; ++i) {
+      const uint4 wv = *reinterpret_cast<const uint4*>(slot + (2 * m + FIRST + i) * kW4TileBytes + lane * 16);
+      words[4 * i] = wv.x;
+      words[4 * i + 1] = wv.y;
+      words[4 * i + 2] = wv.z;
+      words[4 * i + 3] = wv.w;
+    }
+#pragma unroll
+    for (int e = 0; e < kGroups; ++e) {
+      const uint8_t* entry = slot + C::kCodes + (lane >> 2) * C::kLaneEntry +
+                             (m * C::kEntries + (C::kEntries == 1 ? 0 : FIRST * C::kEntries / 2 + e)) * C::kEntryBytes;
+      float s0, s1, z0 = 1.f, z1 = 16.f;  // of outputs g and g + 8
       if constexpr (C::ZP) {
-        const uint2 sz = *reinterpret_cast<const uint2*>(ent);
-        sc = sz.x;
-        W::zero_consts(sz.y, zg, zg8);
+        const uint2 sz = *reinterpret_cast<const uint2*>(entry);
+        W::pair_f32(sz.x, s0, s1);
+        W::pair_f32(sz.y, z0, z1);
+        z1 *= 16.f;
       } else {
-        sc = *reinterpret_cast<const uint32_t*>(ent);
-        W::zero_consts(W::splat(8.f), zg, zg8);  // folds to constants
+        W::pair_f32(*reinterpret_cast<const uint32_t*>(entry), s0, s1);
       }
+      float part[N][4];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int s = e * kPer + i;
         uint32_t a[4];
-        W::dequant(words[s], zg, zg8, a);
+        w4_operands(words[s], a);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n == 0 || n < n_tok_tiles) {
-            const uint4 xv = xr[n][s >> 1];
-            const uint32_t b0 = (s & 1) ? xv.z : xv.x, b1 = (s & 1) ? xv.w : xv.y;
-            if (i == 0 && (!C::kKeep || HALF == 0))
-              W::template mma<true>(pt[n], a, b0, b1);
-            else
-              W::template mma<false>(pt[n], a, b0, b1);
-          }
+        for (int n = 0; n < N; ++n) {
+          if (i == 0)
+            W::template mma<true>(part[n], a, xr[s][n][0], xr[s][n][1]);
+          else
+            W::template mma<false>(part[n], a, xr[s][n][0], xr[s][n][1]);
         }
       }
-      if (!C::kKeep || HALF == 1) {
-        float s0, s1;
-        W::scales(sc, s0, s1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n == 0 || n < n_tok_tiles) {
-            acc[m][n][0] = fmaf(s0, pt[n][0], acc[m][n][0]);
-            acc[m][n][1] = fmaf(s0, pt[n][1], acc[m][n][1]);
-            acc[m][n][2] = fmaf(s1, pt[n][2], acc[m][n][2]);
-            acc[m][n][3] = fmaf(s1, pt[n][3], acc[m][n][3]);
-          }
-        }
+      for (int n = 0; n < N; ++n) {
+        acc[m][n][0] = fmaf(s0, fmaf(-z0, sum[e][n][0], part[n][0]), acc[m][n][0]);
+        acc[m][n][1] = fmaf(s0, fmaf(-z0, sum[e][n][1], part[n][1]), acc[m][n][1]);
+        acc[m][n][2] = fmaf(s1, fmaf(-z1, sum[e][n][0], part[n][2]), acc[m][n][2]);
+        acc[m][n][3] = fmaf(s1, fmaf(-z1, sum[e][n][1], part[n][3]), acc[m][n][3]);
       }
     }
   }
 }
 
-// The lane's x of one tile: 16 bytes at inputs 32 h + 8 t of each of its
-// tokens; x reads as zero for tokens (xp[n] == nullptr) and tiles that are not.
-template <typename T, int NT>
-__device__ __forceinline__ void w4_load_x(const T* const (&xp)[NT], int tile, bool exists, uint4 (&xr)[NT][2]) {
+// The lane's x of tile `half` of a step: 16 bytes at inputs 32 h + 8 t of each
+// of its tokens; xp[n] is at the step's first input.  (A token that does not
+// exist has the address of one that does: its column of the products is never
+// stored, and no column sees another.)
+template <typename T, int N, int NT>
+__device__ __forceinline__ void w4_load_x(const T* const (&xp)[NT], int half, uint4 (&xr)[NT][2]) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    xr[n][0] = xr[n][1] = make_uint4(0, 0, 0, 0);
-    if (exists && xp[n]) {
-      const T* p = xp[n] + (size_t)tile * kW4Tile;
-      xr[n][0] = *reinterpret_cast<const uint4*>(p);
-      xr[n][1] = *reinterpret_cast<const uint4*>(p + 32);
-    }
+  for (int n = 0; n < N; ++n) {
+    xr[n][0] = *reinterpret_cast<const uint4*>(xp[n] + half * kW4Tile);
+    xr[n][1] = *reinterpret_cast<const uint4*>(xp[n] + half * kW4Tile + 32);
   }
 }
 
-// Accumulators to the CTA's reduction buffer, red[K split][token][row].
-template <typename C>
-__device__ __forceinline__ void w4_store_partials(float* red, int ks, int rg, int lane, int n_tok_tiles,
-                                                  const float (&acc)[kW4Panels][C::NT][4]) {
+// A warp's share [s0, s1) of the steps of K for one item.  x of its first tile
+// is in x.v[0] (loaded before, when there is a step).  `advance` returns once the
+// next step is in its ring slot and refills the slot before; `slot` follows the
+// ring.  One token tile takes both tiles of a step together and has x of the
+// next step on its way meanwhile; more token tiles have registers for one tile
+// ahead only.  N: token tiles that exist.
+template <typename T, typename C>
+struct W4X {
+  uint4 v[C::NT == 1 ? 4 : 2][1][C::NT][2];  // NT == 1: two steps of two tiles; else two tiles
+};
+template <typename T, typename C>
+__device__ __forceinline__ void w4_first_x(const T* const (&xp)[C::NT], bool second, W4X<T, C>& x) {
+  w4_load_x<T, C::NT>(xp, 0, x.v[0][0]);
+  if constexpr (C::NT == 1)
+    if (second) w4_load_x<T, 1>(xp, 1, x.v[1][0]);
+}
+template <typename T, typename C, int N, typename Advance>
+__device__ __forceinline__ void w4_run_tokens(int s0, int s1, int tiles, const uint8_t* ring, uint32_t& slot,
+                                              const T* (&xp)[C::NT], W4X<T, C>& x, int lane,
+                                              float (&acc)[kW4Panels][C::NT][4], Advance& advance) {
+  auto consumed = [&]() { slot = slot + C::kSlot == C::kDepth * C::kSlot ? 0 : slot + C::kSlot; };
+  auto next_x = [&]() {
+#pragma unroll
+    for (int n = 0; n < N; ++n) xp[n] += 2 * kW4Tile;
+  };
+  if constexpr (C::NT == 1) {
+    auto one = [&](int s, uint4 (&c0)[1][1][2], uint4 (&c1)[1][1][2], uint4 (&n0)[1][1][2], uint4 (&n1)[1][1][2]) {
+      next_x();
+      if (s + 1 < s1) {
+        w4_load_x<T, 1>(xp, 0, n0[0]);
+        if (2 * s + 3 < tiles) w4_load_x<T, 1>(xp, 1, n1[0]);
+      }
+      advance();
+      if (2 * s + 1 < tiles) {
+        const uint4 c[2][1][2] = {{{c0[0][0][0], c0[0][0][1]}}, {{c1[0][0][0], c1[0][0][1]}}};
+        w4_tiles<T, C, 1, 0, 2>(ring + slot, c, lane, acc);
+      } else {
+        w4_tiles<T, C, 1, 0, 1>(ring + slot, c0, lane, acc);
+      }
+      consumed();
+    };
+    for (int s = s0; s < s1; s += 2) {
+      one(s, x.v[0], x.v[1], x.v[2], x.v[3]);
+      if (s + 1 >= s1) break;
+      one(s + 1, x.v[2], x.v[3], x.v[0], x.v[1]);
+    }
+  } else {
+    for (int s = s0; s < s1; ++s) {
+      const bool second = 2 * s + 1 < tiles;
+      if (second) w4_load_x<T, N>(xp, 1, x.v[1][0]);
+      advance();
+      w4_tiles<T, C, N, 0, 1>(ring + slot, x.v[0], lane, acc);
+      next_x();
+      if (s + 1 < s1) w4_load_x<T, N>(xp, 0, x.v[0][0]);
+      if (second) w4_tiles<T, C, N, 1, 1>(ring + slot, x.v[1], lane, acc);
+      consumed();
+    }
+  }
+}
+// The same for the token tiles at hand (the same number for the whole warp).
+template <typename T, typename C, typename Advance>
+__device__ __forceinline__ void w4_run(int s0, int s1, int tiles, const uint8_t* ring, uint32_t& slot,
+                                       const T* (&xp)[C::NT], W4X<T, C>& x, int n_tok_tiles, int lane,
+                                       float (&acc)[kW4Panels][C::NT][4], Advance& advance) {
+  if constexpr (C::NT == 1) {
+    w4_run_tokens<T, C, 1>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
+  } else {
+    if (n_tok_tiles == 1)
+      w4_run_tokens<T, C, 1>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
+    else if (C::NT == 2 || n_tok_tiles == 2)
+      w4_run_tokens<T, C, 2>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
+    else
+      w4_run_tokens<T, C, C::NT>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
+  }
+}
+
+// Accumulators, brought back to units of 1, to the warp's sums [token][row].
+template <typename T, typename C>
+__device__ __forceinline__ void w4_store_sums(float* sums, int lane, int n_tok_tiles,
+                                              const float (&acc)[kW4Panels][C::NT][4]) {
   const int g = lane >> 2, t = lane & 3;
+  constexpr float u0 = W4Type<T>::kUnit, u1 = W4Type<T>::kUnit / 16.f;
 #pragma unroll
   for (int n = 0; n < C::NT; ++n) {
     if (n == 0 || n < n_tok_tiles) {
-      float* p = red + ((size_t)ks * C::NT * 8 + n * 8 + 2 * t) * C::kPitch + rg * kW4Rows + g;
+      float* p = sums + (n * 8 + 2 * t) * kW4SumPitch + g;
 #pragma unroll
       for (int m = 0; m < kW4Panels; ++m) {
-        p[m * 16] = acc[m][n][0];
-        p[m * 16 + C::kPitch] = acc[m][n][1];
-        p[m * 16 + 8] = acc[m][n][2];
-        p[m * 16 + 8 + C::kPitch] = acc[m][n][3];
+        p[m * 16] = u0 * acc[m][n][0];
+        p[m * 16 + kW4SumPitch] = u0 * acc[m][n][1];
+        p[m * 16 + 8] = u1 * acc[m][n][2];
+        p[m * 16 + 8 + kW4SumPitch] = u1 * acc[m][n][3];
       }
     }
   }
 }
 
-// Sum of the K splits' partials of (token, row), in their order.
+// Sum over the K splits, in their order, of element `at` of their warps' sums.
 template <typename C>
-__device__ __forceinline__ float w4_sum_partials(const float* red, int token, int row) {
+__device__ __forceinline__ float w4_add_splits(const float* const (&sums)[C::KS], int at) {
   float v = 0.f;
 #pragma unroll
-  for (int w = 0; w < C::KS; ++w) v += red[((size_t)w * C::NT * 8 + token) * C::kPitch + row];
+  for (int w = 0; w < C::KS; ++w) v += sums[w][at];
   return v;
 }
 

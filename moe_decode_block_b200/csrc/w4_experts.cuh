@@ -28,6 +28,7 @@ struct W4Phase {
   W4Geom geom;
   int blocks;              // blocks of 64 weight rows of a unit (UP: 32 gate rows and their 32 up rows)
   int items;               // of a unit: ceil(blocks / row groups of a CTA)
+  uint32_t items_inv;      // ceil(2^32 / items) (0 for 1): i / items by one multiplication, exact for i * items < 2^32
   uint32_t up_off;         // UP: bytes from a gate panel to its up panel
   const __nv_bfloat16* x;  // activations [rows, x_cols]
   int x_cols;
@@ -43,12 +44,12 @@ struct W4ExpertArgs {
   const Plan* plan;
 };
 
-// A unit's tokens as seen by one lane.
-template <int NT>
+// An item's unit: loaded one item before the lane's tokens are, which are
+// loaded one item before they are used -- no load of the plan is waited for
+// where it is issued.
 struct W4Unit {
-  int count;    // tokens of the unit
-  int begin;    // shared: first token; routed: first assignment of the plan
-  int row[NT];  // activation row of the lane's token in each tile, -1: none
+  int count;  // tokens, 0: no such item
+  int begin;  // shared: first token; routed: first assignment of the plan
 };
 
 constexpr int kW4ExpertSplit = 4;  // warps that split K; the CTA's other factor of 2 stands in the rows
@@ -60,10 +61,13 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
   using T = __nv_bfloat16;
   extern __shared__ __align__(1024) uint8_t w4_smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int ks = warp % C::KS, rg = warp / C::KS;
+  const int ks = warp % C::KS, rg = warp / C::KS;  // share of K, row group
   uint8_t* ring = w4_smem + (size_t)warp * C::kDepth * C::kSlot;
   const uint32_t ring_addr = smem_addr(ring);
-  float* red = reinterpret_cast<float*>(w4_smem + (size_t)kW4Warps * C::kDepth * C::kSlot);
+  float* sums = reinterpret_cast<float*>(w4_smem + C::kRing);  // the warps' sums of an item
+
+  __shared__ int s_row[2][kMaxUnitTokens];    // output rows of an item's tokens (by item parity)
+  __shared__ float s_wt[2][kMaxUnitTokens];   // DOWN: their routing weights
 
   const int shared_items = a.n_su * a.ph[0].items;
   const int step = gridDim.x;
@@ -79,6 +83,13 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
   // this grid's completion before it reads anything of it
   cudaTriggerProgrammaticLaunchCompletion();
 
+  // phase, unit and block of an item
+  auto place = [&](int item, int& ph, int& u, int& blk) {
+    ph = item >= shared_items;
+    const uint32_t i = item - (ph ? shared_items : 0), inv = a.ph[ph].items_inv;
+    u = inv ? __umulhi(i, inv) : i;
+    blk = (i - u * a.ph[ph].items) * C::RW;
+  };
   // this warp's steps of K in a phase
   auto steps_of = [&](int ph, int& s0, int& s1) {
     const int n = w4_steps(a.ph[ph].geom);
@@ -87,22 +98,34 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
   };
 
   // ---- the weight stream: runs up to kDepth - 1 steps ahead of the products,
-  // over the borders of items
-  int p_item = blockIdx.x, p_slot = 0;
+  // over the borders of items; once the plan is there, the expert of the item
+  // after the stream's present one is on its way early
+  int p_item = blockIdx.x, p_expert = 0;
+  uint32_t p_slot = 0;
+  bool p_known = false;
+  auto p_fetch = [&]() {  // the expert of item p_item
+    p_known = true;
+    if (p_item < shared_items || p_item >= n_items) return;
+    int ph, u, blk;
+    place(p_item, ph, u, blk);
+    p_expert = __ldcg(&a.plan->unit_expert[u]);
+  };
   W4Stream st;
   st.valid = 0xfu;
-  auto p_locate = [&]() {  // the stream's place for item p_item; false: no more
-    for (;; p_item += step) {
+  auto p_locate = [&]() {  // start the stream of item p_item (its expert fetched); false: no more
+    for (;;) {
       if (p_item >= shared_items) read_plan();
       if (p_item >= n_items) return false;
-      const int ph = p_item >= shared_items;
-      const W4Phase& P = a.ph[ph];
-      const int i = p_item - (ph ? shared_items : 0);
-      const int u = i / P.items, b = (i - u * P.items) * C::RW + rg;
-      int s0, s1;
+      int ph, u, b, s0, s1;
+      place(p_item, ph, u, b);
+      b += rg;
       steps_of(ph, s0, s1);
+      const W4Phase& P = a.ph[ph];
+      if (!p_known) p_fetch();
+      const uint8_t* w = ph ? reinterpret_cast<const uint8_t*>(tab.p[p_expert]) : a.shared_w;
+      p_item += step;
+      p_known = false;
       if (s0 >= s1 || b >= P.blocks) continue;  // nothing for this warp
-      const uint8_t* w = ph ? reinterpret_cast<const uint8_t*>(tab.p[__ldcg(&a.plan->unit_expert[u])]) : a.shared_w;
 #pragma unroll
       for (int m = 0; m < kW4Panels; ++m)
         st.off[m] = DOWN ? m * P.geom.panel_bytes : (m & 1) * P.geom.panel_bytes + (m >> 1) * P.up_off;
@@ -111,124 +134,126 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
     }
   };
   bool p_more = p_locate();
+  uint32_t slot = 0;
   auto produce = [&]() {
     if (p_more) {
       w4_stream_step<C, false>(st, ring_addr + p_slot, lane);
-      if (st.left <= 0) {
-        p_item += step;
-        p_more = p_locate();
-      }
+      if (have_plan && !p_known) p_fetch();
+      if (st.left <= 0) p_more = p_locate();
     }
     cp_async_commit();
     p_slot = p_slot + C::kSlot == C::kDepth * C::kSlot ? 0 : p_slot + C::kSlot;
+  };
+  // the next step is in; every lane is done with the slot that is refilled
+  auto advance = [&]() {
+    cp_async_wait<C::kDepth - 2>();
+    __syncwarp();
+    produce();
   };
 #pragma unroll 1
   for (int d = 0; d < C::kDepth - 1; ++d) produce();
 
   // ---- the products
-  auto unit_of = [&](int item, W4Unit<NT>& un) {
+  auto unit_of = [&](int item, W4Unit& un) {
     if (item >= shared_items) read_plan();
-    un.count = 0;
+    un.count = un.begin = 0;
     if (item >= n_items) return;
-    const int ph = item >= shared_items;
-    const int i = item - (ph ? shared_items : 0);
-    const int u = i / a.ph[ph].items;
-    un.begin = ph ? __ldcg(&a.plan->unit_begin[u]) : u * kMaxUnitTokens;
-    un.count = ph ? __ldcg(&a.plan->unit_count[u]) : min(kMaxUnitTokens, a.batch - un.begin);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int t = n * 8 + (lane >> 2);
-      un.row[n] = -1;
-      if (t < un.count) {
-        const int slot = ph ? __ldcg(&a.plan->assign_slot[un.begin + t]) : un.begin + t;
-        un.row[n] = (ph && !DOWN) ? slot / a.top_k : slot;
-      }
+    int ph, u, blk;
+    place(item, ph, u, blk);
+    if (ph) {
+      un.begin = __ldcg(&a.plan->unit_begin[u]);
+      un.count = __ldcg(&a.plan->unit_count[u]);
+    } else {
+      un.begin = u * kMaxUnitTokens;
+      un.count = min(kMaxUnitTokens, a.batch - un.begin);
     }
   };
-  auto rows_of = [&](const W4Unit<NT>& un, int ph, const T* (&xp)[NT]) {
+  // the lane's tokens: row of the activations (routed: the assignment's slot),
+  // the first token's for those that do not exist
+  auto slots_of = [&](const W4Unit& un, bool routed, int (&slot)[NT]) {
+    if (un.count == 0) return;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      xp[n] = un.count > 0 && un.row[n] >= 0
-                  ? a.ph[ph].x + (size_t)un.row[n] * a.ph[ph].x_cols + 8 * (lane & 3)
-                  : nullptr;
+    for (int n = 0; n < NT; ++n) {
+      const int t = n * 8 + (lane >> 2), i = un.begin + (t < un.count ? t : 0);
+      slot[n] = routed ? __ldcg(&a.plan->assign_slot[i]) : i;
+    }
+  };
+  auto rows_of = [&](const int (&slot)[NT], int ph, int s0, const T* (&xp)[NT]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = ph && !DOWN ? (int)((unsigned)slot[n] / (unsigned)a.top_k) : slot[n];
+      xp[n] = a.ph[ph].x + (size_t)row * a.ph[ph].x_cols + s0 * (2 * kW4Tile) + 8 * (lane & 3);
+    }
   };
 
   if constexpr (DOWN) read_plan();  // the activations are complete
-  W4Unit<NT> next;
-  unit_of(blockIdx.x, next);
-  uint4 xa[NT][2], xb[NT][2];
-  int slot = 0;
-  {
+  W4Unit un, next;
+  int next_slot[NT];
+  unit_of(blockIdx.x, un);
+  unit_of(blockIdx.x + step, next);
+  W4X<T, C> xr;
+  const T* xp[NT];
+  int parity = 0;
+  if (un.count > 0) {
     const int ph = (int)blockIdx.x >= shared_items;
     int s0, s1;
     steps_of(ph, s0, s1);
-    const T* xp[NT];
-    rows_of(next, ph, xp);
-    w4_load_x<T, NT>(xp, 2 * s0, s0 < s1, xa);
+    slots_of(un, ph, next_slot);
+    rows_of(next_slot, ph, s0, xp);
+    if (s0 < s1) w4_first_x<T, C>(xp, 2 * s0 + 1 < a.ph[ph].geom.tiles, xr);
   }
   for (int item = blockIdx.x;; item += step) {
     if (item >= shared_items) read_plan();
     if (item >= n_items) break;
-    const int ph = item >= shared_items;
+    int ph, u, b0;  // b0: the item's first block
+    place(item, ph, u, b0);
     const W4Phase& P = a.ph[ph];
-    const W4Unit<NT> un = next;
     const int n_tok_tiles = (un.count + 7) >> 3;
-    const int i = item - (ph ? shared_items : 0);
-    const int b0 = i % P.items * C::RW;  // the item's first block
     int s0, s1;
     steps_of(ph, s0, s1);
     if (b0 + rg >= P.blocks) s1 = s0;  // no rows for this warp
-    const T* xp[NT];
-    rows_of(un, ph, xp);
-    unit_of(item + step, next);
-    float acc[kW4Panels][NT][4] = {};
-    float part[C::kKeep ? kW4Panels : 1][NT][4];
-    for (int s = s0; s < s1; ++s) {
-      w4_load_x<T, NT>(xp, 2 * s + 1, 2 * s + 1 < P.geom.tiles, xb);
-      cp_async_wait<C::kDepth - 2>();
-    __syncwarp();  // every lane's pieces are in; every lane is done with the slot refilled next
-      produce();
-      w4_tile<T, C, 0>(ring + slot, xa, n_tok_tiles, lane, part, acc);
-      w4_load_x<T, NT>(xp, 2 * s + 2, s + 1 < s1, xa);
-      w4_tile<T, C, 1>(ring + slot, xb, n_tok_tiles, lane, part, acc);
-      slot = slot + C::kSlot == C::kDepth * C::kSlot ? 0 : slot + C::kSlot;
+    const int next_ph = item + step >= shared_items;
+    slots_of(next, next_ph, next_slot);
+    W4Unit after;
+    unit_of(item + 2 * step, after);
+    if (warp == 0 && lane < un.count) {
+      s_row[parity][lane] = ph ? __ldcg(&a.plan->assign_slot[un.begin + lane]) : un.begin + lane;
+      if constexpr (DOWN) s_wt[parity][lane] = ph ? __ldcg(&a.plan->assign_w[un.begin + lane]) : 1.f;
     }
+    float acc[kW4Panels][NT][4] = {};
+    w4_run<T, C>(s0, s1, P.geom.tiles, ring, slot, xp, xr, n_tok_tiles, lane, acc, advance);
     if (next.count > 0) {  // the next item's first activations, under this one's epilogue
-      const int nph = item + step >= shared_items;
       int n0, n1;
-      steps_of(nph, n0, n1);
-      const T* np[NT];
-      rows_of(next, nph, np);
-      w4_load_x<T, NT>(np, 2 * n0, n0 < n1, xa);
+      steps_of(next_ph, n0, n1);
+      rows_of(next_slot, next_ph, n0, xp);
+      if (n0 < n1) w4_first_x<T, C>(xp, 2 * n0 + 1 < a.ph[next_ph].geom.tiles, xr);
     }
     __syncthreads();  // the last item's sums have been read
-    w4_store_partials<C>(red, ks, rg, lane, n_tok_tiles, acc);
+    w4_store_sums<T, C>(sums + warp * (C::kSums / 4), lane, n_tok_tiles, acc);
     __syncthreads();
 
-    if constexpr (DOWN) {
-      float* y = static_cast<float*>(P.out) + b0 * kW4Rows;
-      const int rows = min(C::kRows, P.out_cols - b0 * kW4Rows);
-      for (int e = tid; e < un.count * C::kRows; e += kW4Threads) {
-        const int tok = e / C::kRows, row = e % C::kRows;
-        if (row >= rows) continue;
-        const float wt = ph ? __ldcg(&a.plan->assign_w[un.begin + tok]) : 1.f;
-        const int r = ph ? __ldcg(&a.plan->assign_slot[un.begin + tok]) : un.begin + tok;
-        y[(size_t)r * P.out_cols + row] = wt * w4_sum_partials<C>(red, tok, row);
-      }
-    } else {
-      // row group r: 32 gate rows, then their 32 up rows
-      T* o = static_cast<T*>(P.out) + b0 * (kW4Rows / 2);
-      const int cols = min(C::kRows / 2, P.out_cols - b0 * (kW4Rows / 2));
-      for (int e = tid; e < un.count * (C::kRows / 2); e += kW4Threads) {
-        const int tok = e / (C::kRows / 2), col = e % (C::kRows / 2);
-        if (col >= cols) continue;
-        const int r = ph ? __ldcg(&a.plan->assign_slot[un.begin + tok]) : un.begin + tok;
-        const int row = (col / 32) * kW4Rows + col % 32;
-        const float gate = w4_sum_partials<C>(red, tok, row);
-        const float up = w4_sum_partials<C>(red, tok, row + 32);
-        o[(size_t)r * P.out_cols + col] = __float2bfloat16_rn(silu_f32(gate) * up);
+    // thread: a row (of 128) of every second token; UP: a column (of 64) of every fourth
+    constexpr int kOut = DOWN ? C::kRows : C::kRows / 2;
+    const int col = tid % kOut, group = DOWN ? col / kW4Rows : col / 32, row = DOWN ? col % kW4Rows : col % 32;
+    const float* of[C::KS];
+#pragma unroll
+    for (int w = 0; w < C::KS; ++w) of[w] = sums + (group * C::KS + w) * (C::kSums / 4);
+    const int out_col = b0 * (kOut / C::RW) + col;
+    if (out_col < P.out_cols) {
+      for (int tok = tid / kOut; tok < un.count; tok += kW4Threads / kOut) {
+        const size_t at = (size_t)s_row[parity][tok] * P.out_cols + out_col;
+        const float v = w4_add_splits<C>(of, tok * kW4SumPitch + row);
+        if constexpr (DOWN) {
+          static_cast<float*>(P.out)[at] = s_wt[parity][tok] * v;
+        } else {  // 32 gate rows, then their 32 up rows
+          const float up = w4_add_splits<C>(of, tok * kW4SumPitch + row + 32);
+          static_cast<T*>(P.out)[at] = __float2bfloat16_rn(silu_f32(v) * up);
+        }
       }
     }
+    un = next;
+    next = after;
+    parity ^= 1;
   }
 }
 

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
   extern __shared__ __align__(1024) uint8_t w4_smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* ring = w4_smem + (size_t)warp * C::kDepth * C::kSlot;
-  float* red = reinterpret_cast<float*>(w4_smem + (size_t)kW4Warps * C::kDepth * C::kSlot);
+  float* cta_sums = reinterpret_cast<float*>(w4_smem);  // over the ring, once it is empty
 
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -59,34 +59,35 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int t = n * 8 + (lane >> 2);
-    xp[n] = t < n_tok ? static_cast<const T*>(a.x) + (tok0 + t) * a.x_stride + 8 * (lane & 3) : nullptr;
+    xp[n] = static_cast<const T*>(a.x) + (tok0 + (t < n_tok ? t : 0)) * a.x_stride + s0 * (2 * kW4Tile) + 8 * (lane & 3);
   }
 
   const uint32_t ring_addr = smem_addr(ring);
-#pragma unroll
-  for (int d = 0; d < C::kDepth - 1; ++d) {
-    if (s0 + d < s1) w4_stream_step<C, true>(st, ring_addr + d * C::kSlot, lane);
+  uint32_t p_slot = 0, slot = 0;
+  auto produce = [&]() {
+    if (st.left > 0) w4_stream_step<C, true>(st, ring_addr + p_slot, lane);
     cp_async_commit();
-  }
-  float acc[kW4Panels][NT][4] = {};
-  float part[C::kKeep ? kW4Panels : 1][NT][4];
-  uint4 xa[NT][2], xb[NT][2];
-  w4_load_x<T, NT>(xp, 2 * s0, s0 < s1, xa);
-  int slot = 0, ahead = C::kDepth - 1;
-  for (int s = s0; s < s1; ++s) {
-    w4_load_x<T, NT>(xp, 2 * s + 1, 2 * s + 1 < a.geom.tiles, xb);
+    p_slot = p_slot + C::kSlot == C::kDepth * C::kSlot ? 0 : p_slot + C::kSlot;
+  };
+  // the next step is in; every lane is done with the slot that is refilled
+  auto advance = [&]() {
     cp_async_wait<C::kDepth - 2>();
-    __syncwarp();  // every lane's pieces are in; every lane is done with the slot refilled next
-    // the slot read in the last iteration takes the step kDepth - 1 ahead
-    if (s + C::kDepth - 1 < s1) w4_stream_step<C, true>(st, ring_addr + ahead * C::kSlot, lane);
-    cp_async_commit();
-    w4_tile<T, C, 0>(ring + slot * C::kSlot, xa, n_tok_tiles, lane, part, acc);
-    w4_load_x<T, NT>(xp, 2 * s + 2, s + 1 < s1, xa);
-    w4_tile<T, C, 1>(ring + slot * C::kSlot, xb, n_tok_tiles, lane, part, acc);
-    ahead = slot;
-    slot = slot + 1 == C::kDepth ? 0 : slot + 1;
-  }
-  w4_store_partials<C>(red, warp, 0, lane, n_tok_tiles, acc);
+    __syncwarp();
+    produce();
+  };
+#pragma unroll
+  for (int d = 0; d < C::kDepth - 1; ++d) produce();
+  float acc[kW4Panels][NT][4] = {};
+  W4X<T, C> xr;
+  if (s0 < s1) w4_first_x<T, C>(xp, 2 * s0 + 1 < a.geom.tiles, xr);
+  w4_run<T, C>(s0, s1, a.geom.tiles, ring, slot, xp, xr, n_tok_tiles, lane, acc, advance);
+  float* base = reinterpret_cast<float*>(w4_smem + C::kRing);
+  constexpr int kStride = C::kSums / 4;
+  w4_store_sums<T, C>(base + warp * kStride, lane, n_tok_tiles, acc);
+  cp_async_wait<0>();
+  const float* sums[kW4Warps];
+#pragma unroll
+  for (int w = 0; w < kW4Warps; ++w) sums[w] = base + w * kStride;
   __syncthreads();
 
   const int row0 = row_blk * kW4Rows;
@@ -96,26 +97,20 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
     if (a.bias) v += W4Type<T>::to_f32(static_cast<const T*>(a.bias)[n]);
     static_cast<T*>(a.out)[(tok0 + tok) * a.out_stride + n] = W4Type<T>::from_f32(v);
   };
-  if (S == 1) {
-    for (int i = tid; i < n_tok * kW4Rows; i += kW4Threads) {
-      const int tok = i / kW4Rows, row = i % kW4Rows;
-      store(tok, row, w4_sum_partials<C>(red, tok, row));
-    }
-    return;
-  }
-  // this CTA's sum replaces warp 0's partial (each element read and written
-  // by one thread), then every CTA of the cluster adds a share of them
   for (int i = tid; i < n_tok * kW4Rows; i += kW4Threads) {
     const int tok = i / kW4Rows, row = i % kW4Rows;
-    const float v = w4_sum_partials<C>(red, tok, row);
-    red[tok * C::kPitch + row] = v;
+    const float v = w4_add_splits<C>(sums, tok * kW4SumPitch + row);
+    if (S == 1)
+      store(tok, row, v);
+    else
+      cta_sums[i] = v;
   }
-  cluster.sync();
+  if (S == 1) return;
+  cluster.sync();  // then every CTA of the cluster adds a share of them
   for (int i = rank * kW4Threads + tid; i < n_tok * kW4Rows; i += S * kW4Threads) {
-    const int tok = i / kW4Rows, row = i % kW4Rows;
     float v = 0.f;
-    for (int r = 0; r < S; ++r) v += cluster.map_shared_rank(red, r)[tok * C::kPitch + row];
-    store(tok, row, v);
+    for (int r = 0; r < S; ++r) v += cluster.map_shared_rank(cta_sums, r)[i];
+    store(i / kW4Rows, i % kW4Rows, v);
   }
   cluster.sync();  // no CTA leaves while another reads its sums
 }

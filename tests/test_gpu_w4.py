@@ -13,7 +13,7 @@ import oracle
 from moe_decode_block_b200 import MOE_OK, MoEDecode, MoEDecodeError, reduce_residual, router_topk_noalloc, synth, w4
 from gpu_helpers import W_ATOL, margin_x
 from w4_reference import TINY as TINY_STEP
-from w4_reference import U, assert_within, dequant64, product_tolerance, random_w4
+from w4_reference import U, assert_within, dequant64, product_magnitude, product_tolerance, random_w4
 
 pytestmark = pytest.mark.gpu
 
@@ -26,10 +26,10 @@ def _x(b, k, dtype, seed):
 def _check_linear(x, codes, scales, zeros, bias, out):
     w = dequant64(codes, scales, zeros)
     y = x.double() @ w.T
-    mag = x.double().abs() @ w.abs().T
+    mag = product_magnitude(x, codes, scales, zeros)
     if bias is not None:
         y, mag = y + bias.double(), mag + bias.double().abs()
-    tol = U[x.dtype] * y.abs() + (1 + U[x.dtype]) * product_tolerance(x.shape[1]) * mag + TINY_STEP[x.dtype]
+    tol = U[x.dtype] * y.abs() + (1 + U[x.dtype]) * product_tolerance(x.shape[1], x.dtype) * mag + TINY_STEP[x.dtype]
     assert_within(out, y, tol)
 
 
@@ -114,23 +114,37 @@ def test_linear_strided_rows_and_untouched_neighbours():
     _check_linear(x1, codes, scales, z, None, out)
 
 
-def test_linear_infinities_and_nan_stay_with_their_token():
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_linear_infinities_and_nan_stay_with_their_token(dtype):
+    """NaN, and an infinity (infinity minus infinity), make their token NaN and no other."""
     b, n, k = 5, 48, 256
-    codes, scales, z = random_w4(n, k, 128, False, torch.bfloat16, seed=3)
-    x = _x(b, k, torch.bfloat16, seed=4)
+    codes, scales, z = random_w4(n, k, 128, False, dtype, seed=3)
+    x = _x(b, k, dtype, seed=4)
     packed = w4.pack(codes, scales, z)
-    clean = torch.empty(b, n, dtype=torch.bfloat16, device="cuda")
+    clean = torch.empty(b, n, dtype=dtype, device="cuda")
     w4.linear(x, packed, clean, 128)
     x[1, 10] = float("nan")
     x[3, 77] = float("inf")
     out = torch.empty_like(clean)
     w4.linear(x, packed, out, 128)
-    w = dequant64(codes, scales, z)
     for t in (0, 2, 4):
         assert torch.equal(out[t], clean[t])
-    assert bool(out[1].isnan().all())
-    want = torch.where(w[:, 77] == 0, torch.tensor(float("nan"), device="cuda", dtype=torch.float64), torch.sign(w[:, 77]) * float("inf"))
-    assert torch.equal(out[3].double().nan_to_num(nan=5.0), want.nan_to_num(nan=5.0))
+    assert bool(out[1].isnan().all()) and bool(out[3].isnan().all())
+
+
+@pytest.mark.parametrize("dtype,lo,hi", [(torch.bfloat16, -50, 50), (torch.float16, -20, 8)])
+def test_linear_activations_of_many_magnitudes(dtype, lo, hi):
+    """Rows of |x| about 2^lo .. 2^hi, and one row that mixes them."""
+    n, k = 40, 512
+    codes, scales, z = random_w4(n, k, 64, True, dtype, seed=13)
+    x = _x(17, k, torch.float32, seed=14)
+    e = torch.linspace(lo, hi, 16, device="cuda").round()
+    x[:16] *= torch.exp2(e)[:, None]
+    x[16] *= torch.exp2(e.repeat(k // 16) - hi)
+    x = x.to(dtype)
+    out = torch.empty(17, n, dtype=dtype, device="cuda")
+    w4.linear(x, w4.pack(codes, scales, z), out, 64, zeros=True)
+    _check_linear(x, codes, scales, z, None, out)
 
 
 def test_linear_same_bits_graph_streams_and_empty_batch():
@@ -198,7 +212,7 @@ class W4Block:
             xr = xd[rows]
             a13, a2 = dequant64(*w13), dequant64(*w2)
             h = xr @ a13.T
-            dh = product_tolerance(H) * (xr.abs() @ a13.abs().T)
+            dh = product_tolerance(H) * product_magnitude(xr, *w13)
             g, u, dg, du = h[:, :inter], h[:, inter:], dh[:, :inter], dh[:, inter:]
             sig = torch.sigmoid(g)
             a = g * sig * u
@@ -206,8 +220,7 @@ class W4Block:
             da = 1.1 * dg * (u.abs() + du) + (g * sig).abs() * du + 2.0 ** -20 * a.abs()
             da = da + U[torch.bfloat16] * (a.abs() + da)  # stored in bf16
             y[rows] += weight * (a @ a2.T)
-            mag = a.abs() @ a2.abs().T
-            tol[rows] += weight * (da @ a2.abs().T + product_tolerance(inter) * (mag + da @ a2.abs().T) + 2.0 ** -23 * mag)
+            tol[rows] += weight * (da @ a2.abs().T + (product_tolerance(inter) + 2.0 ** -23) * product_magnitude(a.abs() + da, *w2))
 
         for e in torch.unique(ids).tolist():
             t, j = (ids == e).nonzero(as_tuple=True)
