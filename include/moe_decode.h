@@ -370,6 +370,16 @@ int moe_w4_linear(const void* x, const void* packed, const void* bias, void* out
                   int32_t dtype, void* stream);
 
 /*
+ * Device status of moe_w4_linear on the current device: synchronises
+ * `stream`, reads the status word that all calls on the device share and
+ * clears it.  MOE_OK, or MOE_ERR_DEVICE_TIMEOUT when a bounded wait of a call
+ * (of more than 16 tokens: smaller ones wait for nothing) gave up, whose
+ * output is then wrong; MOE_ERR_NO_DEVICE, MOE_ERR_ARCH, MOE_ERR_CUDA.  Not
+ * while `stream` is being captured.
+ */
+int moe_w4_linear_status(void* stream);
+
+/*
  * moe_decode_forward with 4-bit expert weights (a handle created with
  * MOE_FLAG_W4_WEIGHTS).  x, router_w, out, topk_ids, topk_w and batch as for
  * moe_decode_forward; four kernels on `stream`.

@@ -6,6 +6,11 @@
 
 #include "moe_host.h"
 #include "w4_core.cuh"
+#include "w4_tc.cuh"
+
+// Status word of the tensor-memory kernel's bounded waits (moe_w4_linear_status):
+// set when a wait gives up, otherwise untouched, so calls may share it.
+static __device__ int g_w4_linear_status;
 
 namespace moe {
 
@@ -115,6 +120,92 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
   cluster.sync();  // no CTA leaves while another reads its sums
 }
 
+// More than 16 tokens: 256 outputs x up to 64 tokens on tcgen05 (w4_tc.cuh); the
+// CTAs of a cluster split K as above.
+template <typename T>
+struct W4LinearItems {
+  const W4LinearArgs& a;
+  W4TcItem item;
+  bool given;
+  __device__ bool next(W4TcItem& it) {
+    if (given) return false;
+    given = true;
+    it = item;
+    return true;
+  }
+  __device__ const W4Geom& geom() const { return a.geom; }
+  __device__ const T* rows() const { return static_cast<const T*>(a.x); }
+  __device__ long long row_offset(const W4TcItem&, int t) const { return t * a.x_stride; }
+};
+
+template <typename T, int GROUP, bool ZP>
+__global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __grid_constant__ W4LinearArgs a) {
+  extern __shared__ __align__(1024) uint8_t w4_smem[];
+  __shared__ W4TcBars bars;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int row0 = (int)(blockIdx.x / S) * kTcRows;
+
+  // K in pairs of tiles between the CTAs: each has some (cluster_for_tc)
+  const int pairs = (a.geom.tiles + 1) / 2;
+  W4LinearItems<T> items{a, {}, false};
+  items.item.tile0 = 2 * (pairs * rank / S);
+  items.item.tile1 = min(a.geom.tiles, 2 * (pairs * (rank + 1) / S));
+  items.item.n_tok = a.batch;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const int p = row0 / 16 + 8 * m;
+    items.item.n_panels[m] = max(0, min(8, a.n_panels - p));
+    items.item.panel[m] = a.w + (size_t)(p < a.n_panels ? p : 0) * a.geom.panel_bytes;
+  }
+  // the rows' sums [token][row], over the B operands: the last MMAs have read them
+  float* exch = reinterpret_cast<float*>(w4_smem + kTcB);
+  static_assert(kTcSlots * kTcBSlot >= kTcTokens * kTcRows * 4, "rows' sums");
+  auto store = [&](int tok, int row, float v) {
+    const int n = row0 + row;
+    if (n >= a.n_out) return;
+    if (a.bias) v += W4Type<T>::to_f32(static_cast<const T*>(a.bias)[n]);
+    static_cast<T*>(a.out)[tok * a.out_stride + n] = W4Type<T>::from_f32(v);
+  };
+
+  w4_tc_begin(bars, kTcWaitLimit);
+  int* status = &g_w4_linear_status;
+  if (warp < kTcUnpackers) {
+    w4_tc_unpack<T, GROUP, ZP>(w4_smem, bars, items, warp, status);
+  } else if (warp < kTcMmaWarp) {
+    const int row = (warp - kTcUnpackers) * 32 + lane;
+    w4_tc_finish(bars, items, warp - kTcUnpackers, status,
+                 [&](const W4TcItem& it, int c, const float (&lo)[16], const float (&hi)[16]) {
+#pragma unroll
+                   for (int n = 0; n < 16; ++n) {
+                     if (c + n < it.n_tok) {
+                       if (S == 1) {
+                         store(c + n, row, lo[n]);
+                         store(c + n, row + 128, hi[n]);
+                       } else {
+                         exch[(c + n) * kTcRows + row] = lo[n];
+                         exch[(c + n) * kTcRows + row + 128] = hi[n];
+                       }
+                     }
+                   }
+                 });
+  } else if (warp == kTcMmaWarp) {
+    w4_tc_mma<T>(w4_smem, bars, items, status);
+  } else {
+    w4_tc_stage<T>(w4_smem, bars, items, warp - kTcMmaWarp - 1, status);
+  }
+  w4_tc_end(bars);
+  if (S == 1) return;
+  cluster.sync();
+  for (int i = rank * kW4TcThreads + tid; i < a.batch * kTcRows; i += S * kW4TcThreads) {
+    float v = 0.f;
+    for (int r = 0; r < S; ++r) v += cluster.map_shared_rank(exch, r)[i];
+    store(i / kTcRows, i % kTcRows, v);
+  }
+  cluster.sync();  // no CTA leaves while another reads its sums
+}
+
 // Plain codes to the packed layout: a thread builds one 32-bit word, another
 // range of threads the group entries.  Outputs behind the last one get codes,
 // scales and zero points of 0.
@@ -183,10 +274,25 @@ int launch_linear(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) 
 }
 
 template <typename T, int GROUP, bool ZP>
+int launch_linear_tc(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) {
+  static std::atomic<uint64_t> raised{0};
+  const auto kern = w4_linear_tc_kernel<T, GROUP, ZP>;
+  const int rc = host_raise_smem(kern, kTcSmem, dev, raised);
+  if (rc != MOE_OK) return rc;
+  const int row_blocks = (a.n_panels * 16 + kTcRows - 1) / kTcRows;
+  // as many CTAs for K as fit one to an SM, with a step each at least
+  int s = 1;
+  while (s < 8 && 2 * s * row_blocks <= num_sms && a.geom.tiles >= 4 * s) s *= 2;
+  const cudaError_t e =
+      host_launch(kern, dim3((unsigned)(row_blocks * s)), kW4TcThreads, kTcSmem, st, s, false, a);
+  return e == cudaSuccess ? MOE_OK : host_fail_cuda(e);
+}
+
+template <typename T, int GROUP, bool ZP>
 int pick_nt(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) {
   if (a.batch <= 8) return launch_linear<T, 1, GROUP, ZP>(a, dev, num_sms, st);
   if (a.batch <= 16) return launch_linear<T, 2, GROUP, ZP>(a, dev, num_sms, st);
-  return launch_linear<T, 4, GROUP, ZP>(a, dev, num_sms, st);
+  return launch_linear_tc<T, GROUP, ZP>(a, dev, num_sms, st);
 }
 
 template <typename T>
@@ -262,6 +368,21 @@ int moe_w4_linear(const void* x, const void* packed, const void* bias, void* out
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return dtype == MOE_DTYPE_BF16 ? pick_linear<__nv_bfloat16>(a, group, has_zeros != 0, dev, sms, st)
                                  : pick_linear<__half>(a, group, has_zeros != 0, dev, sms, st);
+}
+
+int moe_w4_linear_status(void* stream) {
+  using namespace moe;
+  int dev, sms;
+  const int rc = host_current_device(&dev, &sms);
+  if (rc != MOE_OK) return rc;
+  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  int st = 0;
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&st, g_w4_linear_status, sizeof st);
+  if (e != cudaSuccess) return host_fail_cuda(e);
+  if (st == kStatusOk) return MOE_OK;
+  const int zero = kStatusOk;
+  if ((e = cudaMemcpyToSymbol(g_w4_linear_status, &zero, sizeof zero)) != cudaSuccess) return host_fail_cuda(e);
+  return MOE_ERR_DEVICE_TIMEOUT;
 }
 
 }  // extern "C"

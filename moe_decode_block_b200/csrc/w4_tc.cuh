@@ -1,0 +1,481 @@
+// w4_tc.cuh -- products of 17 to 64 tokens with a 4-bit weight matrix on the
+// 5th-generation tensor cores.
+//
+// mma.sync takes a token tile of 8 per instruction and does 1,024 products a
+// clock and SM whatever it is given (measured: 976), so at 64 tokens it stops at
+// 16 weights a clock and SM where HBM delivers 46.  tcgen05.mma takes all tokens
+// at once: 128 weight rows x up to 64 tokens x 16 inputs in 45 clocks (measured,
+// the same for 16, 32 and 64 tokens; the weights in tensor memory), 45 weights a
+// clock.
+//
+// Mathematics.  Here a weight s (q - z) is rounded once to the activations' type
+// (half a step: 2^-9 relative in bf16, 2^-12 in fp16; powers of two times s are
+// exact) and the products are summed in fp32 over all of K in tensor memory.  The
+// exact form of w4_core.cuh -- a group's sum read back and scaled in fp32 -- was
+// built too: reading 64 sums a row back every 128 inputs, beside the MMAs' own
+// traffic to tensor memory, took 1,700 clocks a step where the MMAs take 860,
+// 52 us for a layer of 16,384 x 7,168 at 64 tokens against MEASURED_US.  The
+// rounding adds 6e-4 to the 1.7e-3 that rounding the result to bf16 costs.
+//
+// A code becomes an operand by a mask (a subnormal, as in w4_core.cuh), one fused
+// multiply-add -- (q - z) times a power of two, exact -- and one product with the
+// scale times the inverse power.
+//
+// Layout of the work.  A CTA has 256 weight rows (two accumulators of 128) and up
+// to 64 tokens, and takes K in steps of 128 inputs.  Its 24 warps:
+//   16 unpackers  each streams one panel through its own ring of asynchronous
+//                 copies and stores its operands to tensor memory with the
+//                 16x256b shape, whose fragment order is the packed layout's;
+//   4 finishers   read an item's sums out of tensor memory (a thread is a row of
+//                 both accumulators) while the next item's are formed;
+//   1 MMA warp    one thread issues a step's tcgen05.mma and commits;
+//   3 stagers     each every third step: the tokens' activations to shared memory
+//                 as the B operand, by asynchronous copies of 8 bytes (K-major
+//                 cores of 8 tokens x 8 inputs; 8-byte pieces move so that the
+//                 inputs' order is the A operand's).
+// Tensor memory: two buffers of sums (by item) and two of operands (by step), 512
+// columns.  Every wait is bounded: a wait that runs out sets the status word and
+// the CTA's abort flag, and the CTA leaves after its own copies and MMAs in
+// flight have ended.
+#pragma once
+
+#include "moe_device.cuh"
+#include "w4_core.cuh"
+
+namespace moe {
+
+constexpr int kTcUnpackers = 16, kTcFinishers = 4, kTcStagers = 3;
+constexpr int kTcMmaWarp = kTcUnpackers + kTcFinishers;
+constexpr int kW4TcThreads = 32 * (kTcMmaWarp + 1 + kTcStagers);
+constexpr int kTcRows = 256;     // weight rows of a CTA
+constexpr int kTcTokens = 64;
+constexpr int kTcStep = 128;     // inputs of a step
+constexpr int kTcRingTiles = 8;  // of an unpacker's ring: 512 bytes each
+constexpr int kTcRingBytes = kTcRingTiles * kW4TileBytes;
+constexpr int kTcSlots = 2 * kTcStagers;            // B operand slots: two for each stager
+constexpr int kTcBSlot = kTcTokens * kTcStep * 2;   // bytes
+constexpr int kTcB = kTcUnpackers * kTcRingBytes;   // offset of the B operands
+constexpr int kTcSmem = kTcB + kTcSlots * kTcBSlot;
+constexpr uint32_t kTcOperandCol = 256;             // first tensor-memory column of the A operands
+
+struct W4TcBars {
+  uint64_t a_full[2], a_empty[2], d_full[2], d_empty[2], b_full[kTcSlots], b_empty[kTcSlots], drained;
+  uint32_t tmem;
+  int ctl[2];  // abort flag, wait limit
+};
+
+// What one CTA multiplies: 16 panels, tiles [tile0, tile1) of K (tile0 even), n_tok tokens.
+struct W4TcItem {
+  const uint8_t* panel[2];  // first panel of each 128 rows
+  int n_panels[2];          // panels that exist of each 8
+  int tile0, tile1, n_tok;
+  __device__ __forceinline__ int steps() const { return (tile1 - tile0 + 1) / 2; }
+};
+
+__device__ __forceinline__ void tc5_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc5_dealloc(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] x B[smem]: kind::f16, one CTA
+__device__ __forceinline__ void tc5_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc5_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+// Fragments of 8 columns each (output g: columns 2 t, 2 t + 1, then g + 8's) of
+// 16 lanes; N of them.
+template <int N>
+__device__ __forceinline__ void tc5_store_operands(uint32_t addr, const uint32_t (&r)[4 * N]) {
+  static_assert(N == 2 || N == 4, "fragments");
+  if constexpr (N == 4)
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// 16 columns of this warp's 32 lanes (a thread is a lane); the wait that defines
+// them comes with the load.
+__device__ __forceinline__ void tc5_load16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// K-major operand without swizzle: cores of 8 rows x 16 bytes; lbo between cores
+// along K, sbo between groups of 8 rows.
+__device__ __forceinline__ uint64_t tc5_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+}
+// fp32 sums, A and B of one 16-bit type, both K-major, M = 128
+template <typename T>
+__device__ __forceinline__ uint32_t tc5_idesc(int n) {
+  const uint32_t type = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// Wait of a whole warp for the phase of `bar` with the given parity.  A phase
+// that has passed already costs one probe and one vote (40 clocks; the loop
+// below with its checks took 90 to 500, and three of them a step were half of the
+// MMA warp's time).  A probe of the loop may suspend the warp for 20 us.  After
+// ctl[1] of them, or once the CTA's abort flag ctl[0] is up, the wait gives up
+// (status word, abort flag) and returns false.
+__device__ __noinline__ bool tc_wait_long(uint32_t bar, uint32_t parity, int* status, volatile int* ctl) {
+  bool ok = false;
+  for (int i = 0; i < ctl[1]; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    ok = __all_sync(0xffffffffu, done != 0);
+    if (ok || __any_sync(0xffffffffu, ctl[0] != 0)) break;
+  }
+  if (!ok) {
+    atomicCAS(status, kStatusOk, kStatusTimeout);
+    ctl[0] = 1;
+  }
+  return ok;
+}
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* ctl) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return tc_wait_long(smem_addr(bar), parity, status, ctl);
+}
+// Probes of a wait by default: 2/3 s.
+constexpr int kTcWaitLimit = 1 << 15;
+
+// A wait of one thread (the MMA warp's), bounded as tc_wait.
+__device__ __forceinline__ bool tc_wait_one(uint64_t* bar, uint32_t parity, int* status, volatile int* ctl) {
+  if (mbar_try_wait(bar, parity)) return true;
+  for (int i = 0; i < ctl[1]; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (ctl[0]) return false;
+  }
+  atomicCAS(status, kStatusOk, kStatusTimeout);
+  ctl[0] = 1;
+  return false;
+}
+
+__device__ __forceinline__ int tc_columns(int n_tok) { return (n_tok + 15) / 16 * 16; }
+
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Codes as subnormals to weights: t = (q - z) 2^-k by one exact fused
+// multiply-add, then t (s 2^k).  k: 6 for outputs g, 2 for outputs g + 8, whose
+// codes stand four bits higher (bf16: 2^-133 q 2^127); in fp16 codes are 2^-24
+// and the factor 2^15: k = 9 and 5.
+template <typename T>
+struct W4Dequant;
+template <>
+struct W4Dequant<__nv_bfloat16> {
+  using V = __nv_bfloat162;
+  static constexpr float kUp = 0x1p+127f, kLow = 0x1p-6f, kHigh = 0x1p-2f;
+  static __device__ __forceinline__ V make(float v) { return __float2bfloat162_rn(v); }
+};
+template <>
+struct W4Dequant<__half> {
+  using V = __half2;
+  static constexpr float kUp = 0x1p+15f, kLow = 0x1p-9f, kHigh = 0x1p-5f;
+  static __device__ __forceinline__ V make(float v) { return __float2half2_rn(v); }
+};
+
+// Before the roles: barriers and tensor memory.  All threads.
+__device__ __forceinline__ void w4_tc_begin(W4TcBars& bars, int limit) {
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.a_full[i], kTcUnpackers);
+      mbar_init(&bars.a_empty[i], 1);
+      mbar_init(&bars.d_full[i], 1);
+      mbar_init(&bars.d_empty[i], kTcFinishers);
+    }
+    for (int i = 0; i < kTcSlots; ++i) {
+      mbar_init(&bars.b_full[i], 1);
+      mbar_init(&bars.b_empty[i], 1);
+    }
+    mbar_init(&bars.drained, 1);
+    bars.ctl[0] = 0;
+    bars.ctl[1] = limit;
+    mbar_fence_init();
+  }
+  if (tid >> 5 == kTcMmaWarp) tc5_alloc(&bars.tmem, 512);
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+}
+// After them.
+__device__ __forceinline__ void w4_tc_end(W4TcBars& bars) {
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  if (threadIdx.x >> 5 == kTcMmaWarp) tc5_dealloc(bars.tmem, 512);
+}
+
+// The MMA warp: one thread of it.  `items` gives the CTA's items in order:
+// next(item) is false after the last.
+template <typename T, typename Items>
+__device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, Items items, int* status) {
+  if ((threadIdx.x & 31) == 0) {
+    const uint32_t tmem = bars.tmem;
+    const uint64_t b_first = tc5_desc(smem_addr(smem + kTcB), 128u, kTcStep * 16u);
+    uint32_t ci = 0, slot = 0, slot_phase = 0, item = 0;
+    bool ok = true;
+    W4TcItem it;
+    for (; ok && items.next(it); ++item) {
+      const uint32_t idesc = tc5_idesc<T>(tc_columns(it.n_tok));
+      const uint32_t d = tmem + (item & 1u) * 128u;
+      if (!(ok = tc_wait_one(&bars.d_empty[item & 1u], ((item >> 1) & 1u) ^ 1u, status, bars.ctl))) break;
+      const int steps = it.steps();
+      for (int s = 0; s < steps; ++s, ++ci) {
+        const uint32_t par = ci & 1u;
+        ok = tc_wait_one(&bars.b_full[slot], slot_phase, status, bars.ctl) &&
+             tc_wait_one(&bars.a_full[par], (ci >> 1) & 1u, status, bars.ctl);
+        if (!ok) break;
+        tc5_fence_after();
+        const uint64_t b0 = b_first + (uint64_t)(slot * (uint32_t)(kTcBSlot >> 4));
+        const uint32_t a = tmem + kTcOperandCol + par * 128u;
+        const bool both = it.tile0 + 2 * s + 1 < it.tile1;  // the last step may be one tile
+#pragma unroll
+        for (uint32_t k = 0; k < kTcStep / 16; ++k) {
+          if (k == kW4Tile / 16 && !both) break;
+          tc5_mma(d, a + 8u * k, b0 + 16u * k, idesc, s > 0 || k > 0);
+          tc5_mma(d + 64u, a + 64u + 8u * k, b0 + 16u * k, idesc, s > 0 || k > 0);
+        }
+        tc5_commit(&bars.a_empty[par]);
+        tc5_commit(&bars.b_empty[slot]);
+        if (++slot == kTcSlots) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
+      }
+      tc5_commit(&bars.d_full[item & 1u]);
+    }
+    // every MMA has ended before tensor memory goes back
+    tc5_commit(&bars.drained);
+    mbar_wait_bounded(&bars.drained, 0u, status);
+  }
+  __syncwarp();
+}
+
+// A stager warp (0..2): the B operands of every third step.  `items.rows()` +
+// `items.row_offset(item, token)` is a token's activation row.
+template <typename T, typename Items>
+__device__ __forceinline__ void w4_tc_stage(uint8_t* smem, W4TcBars& bars, Items items, int stager, int* status) {
+  const int lane = threadIdx.x & 31;
+  uint32_t ci = 0;  // step of the item's first
+  // the copies of this warp's last step are handed over once they have landed,
+  // while the next step's are under way
+  uint32_t last = 0;
+  bool pending = false;
+  auto hand_over = [&]() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.b_full[last]);
+  };
+  W4TcItem it;
+  while (items.next(it)) {
+    const int groups = tc_columns(it.n_tok) / 8, steps = it.steps();
+    for (int s = (int)((stager + kTcStagers - ci % kTcStagers) % kTcStagers); s < steps; s += kTcStagers) {
+      const uint32_t i = ci + (uint32_t)s, at = i % kTcSlots;
+      if (!tc_wait(&bars.b_empty[at], ((i / kTcSlots) & 1u) ^ 1u, status, bars.ctl)) {
+        cp_async_wait<0>();
+        return;
+      }
+      // lane: token 8 g + lane % 8 (the first token for those that do not exist),
+      // piece t = lane / 8 of 32 inputs, whose 8-byte halves q go to cores
+      // 2 (2 h + q) + t / 2
+      const int tile = it.tile0 + 2 * s;
+      const T* first = items.rows() + (size_t)tile * kW4Tile + 8 * (lane >> 3);
+      uint32_t dst = smem_addr(smem + kTcB + at * kTcBSlot) + (lane & 7) * 16 + (lane >> 4) * 128 + ((lane >> 3) & 1) * 8;
+      const bool both = tile + 1 < it.tile1;
+      for (int g = 0; g < groups; ++g, dst += kTcStep * 16) {
+        const int t = 8 * g + (lane & 7);
+        const T* p = first + items.row_offset(it, t < it.n_tok ? t : 0);
+#pragma unroll
+        for (int q = 0; q < kTcStep / 32; ++q) {
+          if (q == kW4Tile / 32 && !both) break;
+          cp_async_8(dst + q * 512, p + 32 * q);
+          cp_async_8(dst + q * 512 + 256, p + 32 * q + 4);
+        }
+      }
+      cp_async_commit();
+      if (pending) {
+        cp_async_wait<1>();
+        hand_over();
+      }
+      last = at;
+      pending = true;
+    }
+    ci += (uint32_t)steps;
+  }
+  cp_async_wait<0>();
+  if (pending) hand_over();
+}
+
+// An unpacker warp (0..15): the A operands of one panel.
+template <typename T, int GROUP, bool ZP, typename Items>
+__device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Items items, int unpacker, int* status) {
+  using Q = W4Dequant<T>;
+  using V = typename Q::V;
+  const int lane = threadIdx.x & 31;
+  const int quarter = unpacker & 3, mt = (unpacker >> 2) & 1, my = 2 * quarter + (unpacker >> 3);  // panel of 8
+  const uint32_t a0 =
+      bars.tmem + ((uint32_t)(32 * quarter + 16 * (unpacker >> 3)) << 16) + kTcOperandCol + mt * 64u;
+  uint8_t* ring = smem + unpacker * kTcRingBytes + lane * 16;
+  const uint32_t ring_addr = smem_addr(ring);
+  constexpr int kLaneEntry = ZP ? 8 : 4, kEntryBytes = 8 * kLaneEntry;
+  constexpr int kEntries = kTcStep / GROUP;  // entries of a step
+
+  // ---- the weight stream, over the borders of items (a panel that does not
+  // exist takes the first one: its rows are not stored)
+  Items ahead = items;
+  const uint8_t* code = nullptr;
+  int left = 0;
+  uint32_t p_slot = 0, slot = 0;
+  bool more = true;
+  auto produce = [&]() {
+    if (left == 0 && more) {
+      W4TcItem it;
+      do {
+        more = ahead.next(it);
+      } while (more && it.tile0 >= it.tile1);
+      if (more) {
+        code = it.panel[mt] + (my < it.n_panels[mt] ? (size_t)my * ahead.geom().panel_bytes : 0) +
+               (size_t)it.tile0 * kW4TileBytes + lane * 16;
+        left = it.tile1 - it.tile0;
+      }
+    }
+    if (more) {
+      cp_async_16(ring_addr + p_slot, code);
+      code += kW4TileBytes;
+      --left;
+    }
+    cp_async_commit();
+    p_slot = (p_slot + kW4TileBytes) % kTcRingBytes;
+  };
+  for (int d = 0; d < kTcRingTiles - 1; ++d) produce();
+
+  const V up = Q::make(Q::kUp);
+  uint32_t ci = 0;
+  bool ok = true;
+  W4TcItem it;
+  while (ok && items.next(it)) {
+    const W4Geom& g = items.geom();
+    const uint8_t* entry = it.panel[mt] + (my < it.n_panels[mt] ? (size_t)my * g.panel_bytes : 0) + g.entry_off +
+                           (size_t)(it.tile0 * kW4Tile / GROUP) * kEntryBytes + (lane >> 2) * kLaneEntry;
+    // the lane's scales (and zero points) of a step, asked for one step before
+    uint32_t e_next[kEntries][ZP ? 2 : 1];
+    auto ask = [&](int tile) {
+#pragma unroll
+      for (int e = 0; e < kEntries; ++e) {
+        if (tile * kW4Tile + e * GROUP < it.tile1 * kW4Tile) {
+          e_next[e][0] = *reinterpret_cast<const uint32_t*>(entry + e * kEntryBytes);
+          if constexpr (ZP) e_next[e][1] = *reinterpret_cast<const uint32_t*>(entry + e * kEntryBytes + 4);
+        }
+      }
+      entry += kEntries * kEntryBytes;
+    };
+    ask(it.tile0);
+    for (int tile = it.tile0; tile < it.tile1; tile += 2, ++ci) {
+      // constants of the groups: outputs g and g + 8
+      V sc[kEntries][2], zc[kEntries][2];
+#pragma unroll
+      for (int e = 0; e < kEntries; ++e) {
+        float s0, s1, z0 = 8.f, z1 = 8.f;
+        W4Type<T>::pair_f32(e_next[e][0], s0, s1);
+        if constexpr (ZP) W4Type<T>::pair_f32(e_next[e][1], z0, z1);
+        sc[e][0] = Q::make(s0 * (1.f / Q::kLow));
+        sc[e][1] = Q::make(s1 * (1.f / Q::kHigh));
+        zc[e][0] = Q::make(-z0 * Q::kLow);
+        zc[e][1] = Q::make(-z1 * Q::kHigh);
+      }
+      ask(tile + 2);
+      // the MMAs of two steps ago have read this buffer
+      if (!(ok = tc_wait(&bars.a_empty[ci & 1u], ((ci >> 1) & 1u) ^ 1u, status, bars.ctl))) break;
+      tc5_fence_after();
+      const uint32_t a = a0 + (ci & 1u) * 128u;
+#pragma unroll
+      for (int ti = 0; ti < 2; ++ti) {
+        if (ti == 1 && tile + 1 >= it.tile1) break;
+        cp_async_wait<kTcRingTiles - 2>();
+        produce();
+        const uint4 w4 = *reinterpret_cast<const uint4*>(ring + slot);
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = (ti * kW4Tile + 16 * i) / GROUP;
+          uint32_t o[4];
+          w4_operands(w[i], o);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const V t = __hmul2(__hfma2(*reinterpret_cast<const V*>(&o[j]), up, zc[e][j & 1]), sc[e][j & 1]);
+            r[4 * i + (j >> 1) + 2 * (j & 1)] = *reinterpret_cast<const uint32_t*>(&t);
+          }
+        }
+        tc5_store_operands<4>(a + 32u * ti, r);
+        slot = (slot + kW4TileBytes) % kTcRingBytes;
+      }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc5_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.a_full[ci & 1u]);
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// A finisher warp (0..3).  `take(item, c, lo, hi)` gets the sums of tokens c ..
+// c + 15 of the lane's rows 32 finisher + lane of both accumulators; called for
+// every 16 tokens that there are.
+template <typename Items, typename Take>
+__device__ __forceinline__ void w4_tc_finish(W4TcBars& bars, Items items, int finisher, int* status, Take take) {
+  const uint32_t lanes = (uint32_t)(32 * finisher) << 16;
+  uint32_t item = 0;
+  W4TcItem it;
+  for (; items.next(it); ++item) {
+    if (!tc_wait(&bars.d_full[item & 1u], (item >> 1) & 1u, status, bars.ctl)) return;
+    tc5_fence_after();
+    const uint32_t d = bars.tmem + lanes + (item & 1u) * 128u;
+    for (int c = 0; c < it.n_tok; c += 16) {
+      float lo[16], hi[16];
+      tc5_load16(d + c, lo);
+      tc5_load16(d + 64u + c, hi);
+      take(it, c, lo, hi);
+    }
+    tc5_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.d_empty[item & 1u]);
+  }
+}
+
+}  // namespace moe

@@ -133,3 +133,10 @@ def linear(x, packed, out, group: int, zeros: bool = False, bias=None, stream=No
     if rc:
         _check(rc, "moe_w4_linear")
     return out
+
+
+def linear_status(stream=None) -> int:
+    """Synchronise `stream` and return the device status of the linear() calls
+    on the current device (MOE_OK or an MOE_ERR_* code); clears it."""
+    dev = _current_device()
+    return load_library().moe_w4_linear_status(_current_stream(dev) if stream is None else _stream_handle(stream))
