@@ -177,15 +177,16 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
     const int row = (warp - kTcUnpackers) * 32 + lane;
     w4_tc_finish(bars, items, warp - kTcUnpackers, status,
                  [&](const W4TcItem& it, int c, const float (&lo)[16], const float (&hi)[16]) {
+                   constexpr float unit = W4Dequant<T, ZP>::kUnit;
 #pragma unroll
                    for (int n = 0; n < 16; ++n) {
                      if (c + n < it.n_tok) {
                        if (S == 1) {
-                         store(c + n, row, lo[n]);
-                         store(c + n, row + 128, hi[n]);
+                         store(c + n, row, unit * lo[n]);
+                         store(c + n, row + 128, unit * hi[n]);
                        } else {
-                         exch[(c + n) * kTcRows + row] = lo[n];
-                         exch[(c + n) * kTcRows + row + 128] = hi[n];
+                         exch[(c + n) * kTcRows + row] = unit * lo[n];
+                         exch[(c + n) * kTcRows + row + 128] = unit * hi[n];
                        }
                      }
                    }
@@ -198,10 +199,22 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
   w4_tc_end(bars);
   if (S == 1) return;
   cluster.sync();
-  for (int i = rank * kW4TcThreads + tid; i < a.batch * kTcRows; i += S * kW4TcThreads) {
-    float v = 0.f;
-    for (int r = 0; r < S; ++r) v += cluster.map_shared_rank(exch, r)[i];
-    store(i / kTcRows, i % kTcRows, v);
+  // four rows of a token at a time
+  for (int i = rank * kW4TcThreads + tid; i < a.batch * (kTcRows / 4); i += S * kW4TcThreads) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int r = 0; r < S; ++r) {
+      const float4 p = reinterpret_cast<const float4*>(cluster.map_shared_rank(exch, r))[i];
+      v.x += p.x;
+      v.y += p.y;
+      v.z += p.z;
+      v.w += p.w;
+    }
+    const int tok = i / (kTcRows / 4), row = i % (kTcRows / 4) * 4;
+    store(tok, row, v.x);
+    store(tok, row + 1, v.y);
+    store(tok, row + 2, v.z);
+    store(tok, row + 3, v.w);
   }
   cluster.sync();  // no CTA leaves while another reads its sums
 }

@@ -17,24 +17,25 @@
 // 52 us for a layer of 16,384 x 7,168 at 64 tokens against MEASURED_US.  The
 // rounding adds 6e-4 to the 1.7e-3 that rounding the result to bf16 costs.
 //
-// A code becomes an operand by a mask (a subnormal, as in w4_core.cuh), one fused
-// multiply-add -- (q - z) times a power of two, exact -- and one product with the
-// scale times the inverse power.
+// A code becomes an operand by a mask (a subnormal, as in w4_core.cuh) and, in
+// bf16 without zero points, one fused multiply-add, q (s 2^100) - 8 s 2^-33, whose
+// one rounding is the weight's (times 2^-33, taken off in the end; s below 2^27).
+// Zero points and fp16 take two instructions: (q - z) times a power of two, exact,
+// then the product with the scale times the inverse power (fp16: s below 128).
 //
 // Layout of the work.  A CTA has 256 weight rows (two accumulators of 128) and up
-// to 64 tokens, and takes K in steps of 128 inputs.  Its 24 warps:
-//   16 unpackers  each streams one panel through its own ring of asynchronous
-//                 copies and stores its operands to tensor memory with the
+// to 64 tokens, and takes K in steps of 128 inputs.  Its 16 warps:
+//   8 unpackers   each streams two panels through its own ring of asynchronous
+//                 copies and stores their operands to tensor memory with the
 //                 16x256b shape, whose fragment order is the packed layout's;
 //   4 finishers   read an item's sums out of tensor memory (a thread is a row of
-//                 both accumulators) while the next item's are formed;
+//                 both accumulators);
 //   1 MMA warp    one thread issues a step's tcgen05.mma and commits;
 //   3 stagers     each every third step: the tokens' activations to shared memory
 //                 as the B operand, by asynchronous copies of 8 bytes (K-major
 //                 cores of 8 tokens x 8 inputs; 8-byte pieces move so that the
 //                 inputs' order is the A operand's).
-// Tensor memory: two buffers of sums (by item) and two of operands (by step), 512
-// columns.  Every wait is bounded: a wait that runs out sets the status word and
+// Tensor memory: the sums (128 columns) and three buffers of operands.  Every wait is bounded: a wait that runs out sets the status word and
 // the CTA's abort flag, and the CTA leaves after its own copies and MMAs in
 // flight have ended.
 #pragma once
@@ -44,22 +45,23 @@
 
 namespace moe {
 
-constexpr int kTcUnpackers = 16, kTcFinishers = 4, kTcStagers = 3;
+constexpr int kTcUnpackers = 8, kTcFinishers = 4, kTcStagers = 3;
 constexpr int kTcMmaWarp = kTcUnpackers + kTcFinishers;
 constexpr int kW4TcThreads = 32 * (kTcMmaWarp + 1 + kTcStagers);
 constexpr int kTcRows = 256;     // weight rows of a CTA
 constexpr int kTcTokens = 64;
 constexpr int kTcStep = 128;     // inputs of a step
-constexpr int kTcRingTiles = 8;  // of an unpacker's ring: 512 bytes each
-constexpr int kTcRingBytes = kTcRingTiles * kW4TileBytes;
+constexpr int kTcRingTiles = 8;  // of an unpacker's ring: 2 panels x 512 bytes each
+constexpr int kTcRingBytes = kTcRingTiles * 2 * kW4TileBytes;
 constexpr int kTcSlots = 2 * kTcStagers;            // B operand slots: two for each stager
 constexpr int kTcBSlot = kTcTokens * kTcStep * 2;   // bytes
 constexpr int kTcB = kTcUnpackers * kTcRingBytes;   // offset of the B operands
 constexpr int kTcSmem = kTcB + kTcSlots * kTcBSlot;
-constexpr uint32_t kTcOperandCol = 256;             // first tensor-memory column of the A operands
+constexpr uint32_t kTcOperandCol = 128;             // first tensor-memory column of the A operands
+constexpr uint32_t kTcBufs = 3;                     // operand buffers
 
 struct W4TcBars {
-  uint64_t a_full[2], a_empty[2], d_full[2], d_empty[2], b_full[kTcSlots], b_empty[kTcSlots], drained;
+  uint64_t a_full[kTcBufs], a_empty[kTcBufs], d_full, d_empty, b_full[kTcSlots], b_empty[kTcSlots], drained;
   uint32_t tmem;
   int ctl[2];  // abort flag, wait limit
 };
@@ -82,18 +84,31 @@ __device__ __forceinline__ void tc5_dealloc(uint32_t addr, uint32_t cols) {
 }
 __device__ __forceinline__ void tc5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// D[tmem] (+)= A[tmem] x B[smem]: kind::f16, one CTA
-__device__ __forceinline__ void tc5_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// 1 in one lane of the warp
+__device__ __forceinline__ uint32_t tc5_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// D[tmem] (+)= A[tmem] x B[smem]: kind::f16, one CTA; by the lane whose `lead` is
+// set, with the whole warp in step, so that the operands stay in uniform registers
+__device__ __forceinline__ void tc5_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void tc5_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+__device__ __forceinline__ void tc5_commit(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(lead)
+      : "memory");
 }
 // Fragments of 8 columns each (output g: columns 2 t, 2 t + 1, then g + 8's) of
 // 16 lanes; N of them.
@@ -171,53 +186,81 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* sta
 // Probes of a wait by default: 2/3 s.
 constexpr int kTcWaitLimit = 1 << 15;
 
-// A wait of one thread (the MMA warp's), bounded as tc_wait.
-__device__ __forceinline__ bool tc_wait_one(uint64_t* bar, uint32_t parity, int* status, volatile int* ctl) {
-  if (mbar_try_wait(bar, parity)) return true;
-  for (int i = 0; i < ctl[1]; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (ctl[0]) return false;
-  }
-  atomicCAS(status, kStatusOk, kStatusTimeout);
-  ctl[0] = 1;
-  return false;
-}
-
 __device__ __forceinline__ int tc_columns(int n_tok) { return (n_tok + 15) / 16 * 16; }
 
 __device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Codes as subnormals to weights: t = (q - z) 2^-k by one exact fused
-// multiply-add, then t (s 2^k).  k: 6 for outputs g, 2 for outputs g + 8, whose
-// codes stand four bits higher (bf16: 2^-133 q 2^127); in fp16 codes are 2^-24
-// and the factor 2^15: k = 9 and 5.
-template <typename T>
+// Codes as subnormals to weights.  `low` operands are outputs g's, the others
+// outputs (g + 8)'s, whose codes stand four bits higher.
+template <typename T, bool ZP>
 struct W4Dequant;
-template <>
-struct W4Dequant<__nv_bfloat16> {
+template <bool ZP>
+struct W4Dequant<__nv_bfloat16, ZP> {
   using V = __nv_bfloat162;
-  static constexpr float kUp = 0x1p+127f, kLow = 0x1p-6f, kHigh = 0x1p-2f;
-  static __device__ __forceinline__ V make(float v) { return __float2bfloat162_rn(v); }
+  static constexpr float kUnit = ZP ? 1.f : 0x1p+33f;  // what the sums are multiplied by in the end
+  V mul[2], add[2], sc[2];
+  static __device__ __forceinline__ V pair(float lo, float hi) { return __floats2bfloat162_rn(lo, hi); }
+  static __device__ __forceinline__ V word(uint32_t w) { return *reinterpret_cast<const V*>(&w); }
+  static __device__ __forceinline__ V low(V v) { return __low2bfloat162(v); }
+  static __device__ __forceinline__ V high(V v) { return __high2bfloat162(v); }
+  // an entry: scales of outputs g and g + 8, and their zero points
+  __device__ __forceinline__ void set(uint32_t s, uint32_t z) {
+    if constexpr (ZP) {
+      // 2^-133 q 2^127 - z 2^-6 (outputs g + 8: 2^-2), times s 2^6 (2^2)
+      const V k = __hmul2(word(s), pair(0x1p+6f, 0x1p+2f)), c = __hmul2(word(z), pair(-0x1p-6f, -0x1p-2f));
+      mul[0] = mul[1] = pair(0x1p+127f, 0x1p+127f);
+      add[0] = low(c);
+      add[1] = high(c);
+      sc[0] = low(k);
+      sc[1] = high(k);
+    } else {
+      const V k = __hmul2(word(s), pair(0x1p+100f, 0x1p+96f)), c = __hmul2(word(s), pair(-0x1p-30f, -0x1p-30f));
+      mul[0] = low(k);
+      mul[1] = high(k);
+      add[0] = low(c);
+      add[1] = high(c);
+    }
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t code, int hi) const {
+    V t = __hfma2(word(code), mul[hi], add[hi]);
+    if constexpr (ZP) t = __hmul2(t, sc[hi]);
+    return *reinterpret_cast<const uint32_t*>(&t);
+  }
 };
-template <>
-struct W4Dequant<__half> {
+template <bool ZP>
+struct W4Dequant<__half, ZP> {
   using V = __half2;
-  static constexpr float kUp = 0x1p+15f, kLow = 0x1p-9f, kHigh = 0x1p-5f;
-  static __device__ __forceinline__ V make(float v) { return __float2half2_rn(v); }
+  static constexpr float kUnit = 1.f;
+  V add[2], sc[2];
+  static __device__ __forceinline__ V pair(float lo, float hi) { return __floats2half2_rn(lo, hi); }
+  static __device__ __forceinline__ V word(uint32_t w) { return *reinterpret_cast<const V*>(&w); }
+  __device__ __forceinline__ void set(uint32_t s, uint32_t z) {
+    // 2^-24 q 2^15 - z 2^-9 (outputs g + 8: 2^-5), times s 2^9 (2^5)
+    const V k = __hmul2(word(s), pair(0x1p+9f, 0x1p+5f));
+    const V c = __hmul2(ZP ? word(z) : pair(8.f, 8.f), pair(-0x1p-9f, -0x1p-5f));
+    add[0] = __low2half2(c);
+    add[1] = __high2half2(c);
+    sc[0] = __low2half2(k);
+    sc[1] = __high2half2(k);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t code, int hi) const {
+    const V t = __hmul2(__hfma2(word(code), pair(0x1p+15f, 0x1p+15f), add[hi]), sc[hi]);
+    return *reinterpret_cast<const uint32_t*>(&t);
+  }
 };
 
 // Before the roles: barriers and tensor memory.  All threads.
 __device__ __forceinline__ void w4_tc_begin(W4TcBars& bars, int limit) {
   const int tid = threadIdx.x;
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < (int)kTcBufs; ++i) {
       mbar_init(&bars.a_full[i], kTcUnpackers);
       mbar_init(&bars.a_empty[i], 1);
-      mbar_init(&bars.d_full[i], 1);
-      mbar_init(&bars.d_empty[i], kTcFinishers);
     }
+    mbar_init(&bars.d_full, 1);
+    mbar_init(&bars.d_empty, kTcFinishers);
     for (int i = 0; i < kTcSlots; ++i) {
       mbar_init(&bars.b_full[i], 1);
       mbar_init(&bars.b_empty[i], 1);
@@ -240,49 +283,58 @@ __device__ __forceinline__ void w4_tc_end(W4TcBars& bars) {
   if (threadIdx.x >> 5 == kTcMmaWarp) tc5_dealloc(bars.tmem, 512);
 }
 
-// The MMA warp: one thread of it.  `items` gives the CTA's items in order:
-// next(item) is false after the last.
+// The MMA warp.  `items` gives the CTA's items in order: next(item) is false
+// after the last.  (Issued from a branch of one thread, whose operands have to be
+// moved to uniform registers one by one, a step's 16 took 1,030 clocks instead of
+// ISSUE_CLOCKS.)
 template <typename T, typename Items>
 __device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, Items items, int* status) {
-  if ((threadIdx.x & 31) == 0) {
-    const uint32_t tmem = bars.tmem;
-    const uint64_t b_first = tc5_desc(smem_addr(smem + kTcB), 128u, kTcStep * 16u);
-    uint32_t ci = 0, slot = 0, slot_phase = 0, item = 0;
-    bool ok = true;
-    W4TcItem it;
-    for (; ok && items.next(it); ++item) {
-      const uint32_t idesc = tc5_idesc<T>(tc_columns(it.n_tok));
-      const uint32_t d = tmem + (item & 1u) * 128u;
-      if (!(ok = tc_wait_one(&bars.d_empty[item & 1u], ((item >> 1) & 1u) ^ 1u, status, bars.ctl))) break;
-      const int steps = it.steps();
-      for (int s = 0; s < steps; ++s, ++ci) {
-        const uint32_t par = ci & 1u;
-        ok = tc_wait_one(&bars.b_full[slot], slot_phase, status, bars.ctl) &&
-             tc_wait_one(&bars.a_full[par], (ci >> 1) & 1u, status, bars.ctl);
-        if (!ok) break;
-        tc5_fence_after();
-        const uint64_t b0 = b_first + (uint64_t)(slot * (uint32_t)(kTcBSlot >> 4));
-        const uint32_t a = tmem + kTcOperandCol + par * 128u;
-        const bool both = it.tile0 + 2 * s + 1 < it.tile1;  // the last step may be one tile
+  const uint32_t lead = tc5_elect();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
+  const uint64_t b_first = tc5_desc(smem_addr(smem + kTcB), 128u, kTcStep * 16u);
+  uint32_t buf = 0, buf_phase = 0, slot = 0, slot_phase = 0, item = 0;
+  bool ok = true;
+  W4TcItem it;
+  for (; ok && items.next(it); ++item) {
+    const uint32_t idesc = tc5_idesc<T>(tc_columns(it.n_tok));
+    const uint32_t d = tmem;
+    if (!(ok = tc_wait(&bars.d_empty, (item & 1u) ^ 1u, status, bars.ctl))) break;
+    for (int tile = it.tile0; tile < it.tile1; tile += 2) {
+      ok = tc_wait(&bars.b_full[slot], slot_phase, status, bars.ctl) &&
+           tc_wait(&bars.a_full[buf], buf_phase, status, bars.ctl);
+      if (!ok) break;
+      tc5_fence_after();
+      const uint64_t b0 = b_first + (uint64_t)(slot * (uint32_t)(kTcBSlot >> 4));
+      const uint32_t a = tmem + kTcOperandCol + buf * 128u;
+      const uint32_t more = tile > it.tile0;
 #pragma unroll
-        for (uint32_t k = 0; k < kTcStep / 16; ++k) {
-          if (k == kW4Tile / 16 && !both) break;
-          tc5_mma(d, a + 8u * k, b0 + 16u * k, idesc, s > 0 || k > 0);
-          tc5_mma(d + 64u, a + 64u + 8u * k, b0 + 16u * k, idesc, s > 0 || k > 0);
-        }
-        tc5_commit(&bars.a_empty[par]);
-        tc5_commit(&bars.b_empty[slot]);
-        if (++slot == kTcSlots) {
-          slot = 0;
-          slot_phase ^= 1u;
+      for (uint32_t k = 0; k < kW4Tile / 16; ++k) {
+        tc5_mma(d, a + 8u * k, b0 + 16u * k, idesc, k > 0 ? 1u : more, lead);
+        tc5_mma(d + 64u, a + 64u + 8u * k, b0 + 16u * k, idesc, k > 0 ? 1u : more, lead);
+      }
+      if (tile + 1 < it.tile1) {  // (the last step may be one tile)
+#pragma unroll
+        for (uint32_t k = kW4Tile / 16; k < kTcStep / 16; ++k) {
+          tc5_mma(d, a + 8u * k, b0 + 16u * k, idesc, 1u, lead);
+          tc5_mma(d + 64u, a + 64u + 8u * k, b0 + 16u * k, idesc, 1u, lead);
         }
       }
-      tc5_commit(&bars.d_full[item & 1u]);
+      tc5_commit(&bars.a_empty[buf], lead);
+      tc5_commit(&bars.b_empty[slot], lead);
+      if (++buf == kTcBufs) {
+        buf = 0;
+        buf_phase ^= 1u;
+      }
+      if (++slot == kTcSlots) {
+        slot = 0;
+        slot_phase ^= 1u;
+      }
     }
-    // every MMA has ended before tensor memory goes back
-    tc5_commit(&bars.drained);
-    mbar_wait_bounded(&bars.drained, 0u, status);
+    tc5_commit(&bars.d_full, lead);
   }
+  // every MMA has ended before tensor memory goes back
+  tc5_commit(&bars.drained, lead);
+  if (lead) mbar_wait_bounded(&bars.drained, 0u, status);
   __syncwarp();
 }
 
@@ -333,7 +385,11 @@ __device__ __forceinline__ void w4_tc_stage(uint8_t* smem, W4TcBars& bars, Items
         hand_over();
       }
       last = at;
-      pending = true;
+      pending = i >= kTcStagers;
+      if (!pending) {  // the first: the MMAs are waiting for it
+        cp_async_wait<0>();
+        hand_over();
+      }
     }
     ci += (uint32_t)steps;
   }
@@ -341,24 +397,28 @@ __device__ __forceinline__ void w4_tc_stage(uint8_t* smem, W4TcBars& bars, Items
   if (pending) hand_over();
 }
 
-// An unpacker warp (0..15): the A operands of one panel.
+// An unpacker warp (0..7): the A operands of two panels.
 template <typename T, int GROUP, bool ZP, typename Items>
 __device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Items items, int unpacker, int* status) {
-  using Q = W4Dequant<T>;
-  using V = typename Q::V;
   const int lane = threadIdx.x & 31;
-  const int quarter = unpacker & 3, mt = (unpacker >> 2) & 1, my = 2 * quarter + (unpacker >> 3);  // panel of 8
-  const uint32_t a0 =
-      bars.tmem + ((uint32_t)(32 * quarter + 16 * (unpacker >> 3)) << 16) + kTcOperandCol + mt * 64u;
+  const int quarter = unpacker & 3, mt = unpacker >> 2;
+  const uint32_t a0 = bars.tmem + ((uint32_t)(32 * quarter) << 16) + kTcOperandCol + mt * 64u;
   uint8_t* ring = smem + unpacker * kTcRingBytes + lane * 16;
   const uint32_t ring_addr = smem_addr(ring);
   constexpr int kLaneEntry = ZP ? 8 : 4, kEntryBytes = 8 * kLaneEntry;
   constexpr int kEntries = kTcStep / GROUP;  // entries of a step
+  // this warp's first panel of an item, and the offset of its second (a panel
+  // that does not exist takes another: its rows are not stored)
+  auto panels = [&](const W4TcItem& it, const W4Geom& g, const uint8_t*& p, uint32_t& second) {
+    const int have = it.n_panels[mt] - 2 * quarter;
+    p = it.panel[mt] + (have > 0 ? (size_t)(2 * quarter) * g.panel_bytes : 0);
+    second = have > 1 ? g.panel_bytes : 0u;
+  };
 
-  // ---- the weight stream, over the borders of items (a panel that does not
-  // exist takes the first one: its rows are not stored)
+  // ---- the weight stream, over the borders of items
   Items ahead = items;
   const uint8_t* code = nullptr;
+  uint32_t code2 = 0;
   int left = 0;
   uint32_t p_slot = 0, slot = 0;
   bool more = true;
@@ -369,86 +429,92 @@ __device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Item
         more = ahead.next(it);
       } while (more && it.tile0 >= it.tile1);
       if (more) {
-        code = it.panel[mt] + (my < it.n_panels[mt] ? (size_t)my * ahead.geom().panel_bytes : 0) +
-               (size_t)it.tile0 * kW4TileBytes + lane * 16;
+        panels(it, ahead.geom(), code, code2);
+        code += (size_t)it.tile0 * kW4TileBytes + lane * 16;
         left = it.tile1 - it.tile0;
       }
     }
     if (more) {
       cp_async_16(ring_addr + p_slot, code);
+      cp_async_16(ring_addr + p_slot + kW4TileBytes, code + code2);
       code += kW4TileBytes;
       --left;
     }
     cp_async_commit();
-    p_slot = (p_slot + kW4TileBytes) % kTcRingBytes;
+    p_slot = (p_slot + 2 * kW4TileBytes) % kTcRingBytes;
   };
+#pragma unroll 1
   for (int d = 0; d < kTcRingTiles - 1; ++d) produce();
 
-  const V up = Q::make(Q::kUp);
-  uint32_t ci = 0;
+  uint32_t buf = 0, buf_phase = 0;
   bool ok = true;
   W4TcItem it;
   while (ok && items.next(it)) {
     const W4Geom& g = items.geom();
-    const uint8_t* entry = it.panel[mt] + (my < it.n_panels[mt] ? (size_t)my * g.panel_bytes : 0) + g.entry_off +
-                           (size_t)(it.tile0 * kW4Tile / GROUP) * kEntryBytes + (lane >> 2) * kLaneEntry;
+    const uint8_t* entry;
+    uint32_t entry2;
+    panels(it, g, entry, entry2);
+    entry += g.entry_off + (size_t)(it.tile0 * kW4Tile / GROUP) * kEntryBytes + (lane >> 2) * kLaneEntry;
     // the lane's scales (and zero points) of a step, asked for one step before
-    uint32_t e_next[kEntries][ZP ? 2 : 1];
+    uint32_t e_next[2][kEntries][2];
     auto ask = [&](int tile) {
 #pragma unroll
       for (int e = 0; e < kEntries; ++e) {
         if (tile * kW4Tile + e * GROUP < it.tile1 * kW4Tile) {
-          e_next[e][0] = *reinterpret_cast<const uint32_t*>(entry + e * kEntryBytes);
-          if constexpr (ZP) e_next[e][1] = *reinterpret_cast<const uint32_t*>(entry + e * kEntryBytes + 4);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(entry + p * entry2 + e * kEntryBytes);
+            e_next[p][e][0] = src[0];
+            if constexpr (ZP) e_next[p][e][1] = src[1];
+          }
         }
       }
       entry += kEntries * kEntryBytes;
     };
     ask(it.tile0);
-    for (int tile = it.tile0; tile < it.tile1; tile += 2, ++ci) {
-      // constants of the groups: outputs g and g + 8
-      V sc[kEntries][2], zc[kEntries][2];
+    for (int tile = it.tile0; tile < it.tile1; tile += 2) {
+      W4Dequant<T, ZP> dq[2][kEntries];
 #pragma unroll
-      for (int e = 0; e < kEntries; ++e) {
-        float s0, s1, z0 = 8.f, z1 = 8.f;
-        W4Type<T>::pair_f32(e_next[e][0], s0, s1);
-        if constexpr (ZP) W4Type<T>::pair_f32(e_next[e][1], z0, z1);
-        sc[e][0] = Q::make(s0 * (1.f / Q::kLow));
-        sc[e][1] = Q::make(s1 * (1.f / Q::kHigh));
-        zc[e][0] = Q::make(-z0 * Q::kLow);
-        zc[e][1] = Q::make(-z1 * Q::kHigh);
-      }
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int e = 0; e < kEntries; ++e) dq[p][e].set(e_next[p][e][0], e_next[p][e][1]);
       ask(tile + 2);
-      // the MMAs of two steps ago have read this buffer
-      if (!(ok = tc_wait(&bars.a_empty[ci & 1u], ((ci >> 1) & 1u) ^ 1u, status, bars.ctl))) break;
+      // the MMAs of three steps ago have read this buffer
+      if (!(ok = tc_wait(&bars.a_empty[buf], buf_phase ^ 1u, status, bars.ctl))) break;
       tc5_fence_after();
-      const uint32_t a = a0 + (ci & 1u) * 128u;
+      const uint32_t a = a0 + buf * 128u;
 #pragma unroll
       for (int ti = 0; ti < 2; ++ti) {
         if (ti == 1 && tile + 1 >= it.tile1) break;
         cp_async_wait<kTcRingTiles - 2>();
         produce();
-        const uint4 w4 = *reinterpret_cast<const uint4*>(ring + slot);
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-        uint32_t r[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = (ti * kW4Tile + 16 * i) / GROUP;
-          uint32_t o[4];
-          w4_operands(w[i], o);
+        for (int p = 0; p < 2; ++p) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(ring + slot + p * kW4TileBytes);
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+          uint32_t r[16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const V t = __hmul2(__hfma2(*reinterpret_cast<const V*>(&o[j]), up, zc[e][j & 1]), sc[e][j & 1]);
-            r[4 * i + (j >> 1) + 2 * (j & 1)] = *reinterpret_cast<const uint32_t*>(&t);
+          for (int i = 0; i < 4; ++i) {
+            const W4Dequant<T, ZP>& q = dq[p][(ti * kW4Tile + 16 * i) / GROUP];
+            uint32_t o[4];
+            w4_operands(w[i], o);
+            r[4 * i] = q(o[0], 0);
+            r[4 * i + 1] = q(o[2], 0);
+            r[4 * i + 2] = q(o[1], 1);
+            r[4 * i + 3] = q(o[3], 1);
           }
+          tc5_store_operands<4>(a + ((uint32_t)(16 * p) << 16) + 32u * ti, r);
         }
-        tc5_store_operands<4>(a + 32u * ti, r);
-        slot = (slot + kW4TileBytes) % kTcRingBytes;
+        slot = (slot + 2 * kW4TileBytes) % kTcRingBytes;
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc5_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.a_full[ci & 1u]);
+      if (lane == 0) mbar_arrive(&bars.a_full[buf]);
+      if (++buf == kTcBufs) {
+        buf = 0;
+        buf_phase ^= 1u;
+      }
     }
   }
   cp_async_wait<0>();
@@ -463,9 +529,9 @@ __device__ __forceinline__ void w4_tc_finish(W4TcBars& bars, Items items, int fi
   uint32_t item = 0;
   W4TcItem it;
   for (; items.next(it); ++item) {
-    if (!tc_wait(&bars.d_full[item & 1u], (item >> 1) & 1u, status, bars.ctl)) return;
+    if (!tc_wait(&bars.d_full, item & 1u, status, bars.ctl)) return;
     tc5_fence_after();
-    const uint32_t d = bars.tmem + lanes + (item & 1u) * 128u;
+    const uint32_t d = bars.tmem + lanes;
     for (int c = 0; c < it.n_tok; c += 16) {
       float lo[16], hi[16];
       tc5_load16(d + c, lo);
@@ -474,7 +540,7 @@ __device__ __forceinline__ void w4_tc_finish(W4TcBars& bars, Items items, int fi
     }
     tc5_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.d_empty[item & 1u]);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.d_empty);
   }
 }
 
