@@ -141,7 +141,8 @@ extern "C" {
  * entry points reject such a handle).  Weight-only: router and activations
  * stay bf16.  Needs hidden, inter and shared_inter to be multiples of 64;
  * combinable with MOE_FLAG_PARTIAL_SUM only.  The handle's workspace grows by
- * max_batch * (top_k + n_shared) * hidden * 4 bytes.
+ * max_batch * (top_k + n_shared) * hidden * 4 bytes (and 25 KB for more than
+ * 16 tokens).
  */
 #define MOE_FLAG_W4_WEIGHTS 64u
 typedef struct moe_decode_shapes {
@@ -351,7 +352,10 @@ int moe_w4_pack(const void* codes, const void* scales, const void* zeros, void* 
 /*
  * out[b, n] = round(bias[n] + sum_k x[b, k] * W[n, k]), b < batch: a dense
  * layer on a packed 4-bit matrix for 1 .. MOE_W4_MAX_BATCH tokens.  Products
- * and sums in fp32 (no weight is rounded), one rounding to the type of x.
+ * and sums in fp32, one rounding to the type of x in the end.  Up to 16 tokens
+ * no weight is rounded; above, each weight s (q - z) is rounded once to the type
+ * of x (s below 2^27 in bf16, below 128 in fp16).  An infinite activation may
+ * give NaN; |x| in bf16 is held from 2^-57 to 2^63 up to 16 tokens.
  * Deterministic.  Asynchronous on `stream` of the current device, one kernel,
  * no workspace, nothing kept between calls: calls may overlap on any streams
  * and be captured in CUDA graphs.
@@ -382,14 +386,17 @@ int moe_w4_linear_status(void* stream);
 /*
  * moe_decode_forward with 4-bit expert weights (a handle created with
  * MOE_FLAG_W4_WEIGHTS).  x, router_w, out, topk_ids, topk_w and batch as for
- * moe_decode_forward; four kernels on `stream`.
+ * moe_decode_forward; four kernels on `stream`, seven above 16 tokens.
  *   w13 : HOST array of n_experts device pointers -> packed [2 * inter, hidden]
  *         (outputs [0, inter) the gate, [inter, 2 * inter) the up projection)
  *   w2  : HOST array of n_experts device pointers -> packed [hidden, inter]
  *   shared_w13, shared_w2 : device, packed (NULL iff n_shared == 0)
  *   group, has_zeros : of every matrix; scales (and zero points) in bf16
- * The experts' products are added in a fixed order: the outputs are the same
- * bits on every call with the same routing weights.  Stage counters of
+ * Products and sums in fp32.  Up to 16 tokens no weight is rounded; above, the
+ * shared expert and the experts that more than 16 tokens chose take each
+ * weight s (q - z) rounded once to bf16 (s below 2^27).  The experts' products
+ * are added in a fixed order: the outputs are the same bits on every call with
+ * the same routing weights.  Stage counters of
  * moe_decode_stats are not kept for this path.  Errors: as
  * moe_decode_forward; MOE_ERR_INVALID_ARG also for a handle made without
  * MOE_FLAG_W4_WEIGHTS, MOE_ERR_UNSUPPORTED_SHAPE for a group that does not

@@ -53,7 +53,7 @@ thread_local int g_last_cuda_error = 0;
 // state never destroys them.
 struct WorkspaceLayout {
   size_t status, ticket, router_epoch, logits, plan, h, a, panel_cnt, panel_ready, queue, h_s, a_s, panel_cnt_s, panel_ready_s,
-      queue_s, acc, x_stage, out_stage, ids_stage, w_stage, state_end, maps, stage_counts, w4_y, total;
+      queue_s, acc, x_stage, out_stage, ids_stage, w_stage, state_end, maps, stage_counts, w4_y, w4_split, total;
 };
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -146,6 +146,7 @@ WorkspaceLayout layout_for(const moe_decode_shapes* s) {
   L.stage_counts = take(2 * moe::kNumClasses * sizeof(unsigned long long));
   // 4-bit weights: the products of every (token, choice), then the shared expert's
   L.w4_y = take((s->flags & MOE_FLAG_W4_WEIGHTS) ? B * (k + (s->n_shared ? 1 : 0)) * H * 4 : 0);
+  L.w4_split = take((s->flags & MOE_FLAG_W4_WEIGHTS) && s->max_batch > moe::kW4LightTokens ? sizeof(moe::W4Split) : 0);
   L.total = off;
   return L;
 }
@@ -689,23 +690,32 @@ W4Pick pick_w4_nt(int group, bool zeros) {
     default: return zeros ? w4_pick_of<NT, 128, true, DOWN>() : w4_pick_of<NT, 128, false, DOWN>();
   }
 }
-// The instance for the tokens that a unit can have at this batch.
+// The instance for the tokens that a unit of its own can have at this batch.
 template <bool DOWN>
 W4Pick pick_w4(int batch, int group, bool zeros) {
-  if (batch <= 8) return pick_w4_nt<1, DOWN>(group, zeros);
-  if (batch <= 16) return pick_w4_nt<2, DOWN>(group, zeros);
-  return pick_w4_nt<4, DOWN>(group, zeros);
+  return batch <= 8 ? pick_w4_nt<1, DOWN>(group, zeros) : pick_w4_nt<2, DOWN>(group, zeros);
+}
+template <bool DOWN>
+W4Kernel pick_w4_tc(int group, bool zeros) {
+  switch (group) {
+    case 32: return zeros ? moe::w4_expert_tc_kernel<32, true, DOWN> : moe::w4_expert_tc_kernel<32, false, DOWN>;
+    case 64: return zeros ? moe::w4_expert_tc_kernel<64, true, DOWN> : moe::w4_expert_tc_kernel<64, false, DOWN>;
+    default: return zeros ? moe::w4_expert_tc_kernel<128, true, DOWN> : moe::w4_expert_tc_kernel<128, false, DOWN>;
+  }
 }
 
 int set_w4_attrs() {
   cudaError_t e;
-  for (int batch : {8, 16, 32})
-    for (int group : {32, 64, 128})
-      for (bool zeros : {false, true}) {
+  for (int group : {32, 64, 128})
+    for (bool zeros : {false, true}) {
+      for (int batch : {8, 16}) {
         const W4Pick up = pick_w4<false>(batch, group, zeros), down = pick_w4<true>(batch, group, zeros);
         if ((e = raise_smem_limit(up.kern, up.smem)) != cudaSuccess) return fail_cuda(e);
         if ((e = raise_smem_limit(down.kern, down.smem)) != cudaSuccess) return fail_cuda(e);
       }
+      if ((e = raise_smem_limit(pick_w4_tc<false>(group, zeros), moe::kTcSmem)) != cudaSuccess) return fail_cuda(e);
+      if ((e = raise_smem_limit(pick_w4_tc<true>(group, zeros), moe::kTcSmem)) != cudaSuccess) return fail_cuda(e);
+    }
   return MOE_OK;
 }
 
@@ -736,61 +746,88 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
     return fail_cuda(err);
   };
   auto mark = [&](int i) { return h->timing ? cudaEventRecord(h->tev[i], sm) : cudaSuccess; };
+  int kernels = 0;
 
   float* y = h->at<float>(h->L.w4_y);
   float* y_s = y + (size_t)batch * s.top_k * s.hidden;
-  moe::W4ExpertArgs up{}, down{};
-  up.n_su = down.n_su = shared_units(s, batch);
-  up.batch = down.batch = batch;
-  up.top_k = down.top_k = s.top_k;
-  up.plan = down.plan = h->at<Plan>(h->L.plan);
-  up.shared_w = static_cast<const uint8_t*>(shared_w13);
-  down.shared_w = static_cast<const uint8_t*>(shared_w2);
+  const Plan* plan = h->at<Plan>(h->L.plan);
+  moe::W4Split* split = h->at<moe::W4Split>(h->L.w4_split);
+  const bool two = batch > moe::kW4LightTokens;  // experts of many tokens apart
   auto inverse = [](int d) { return d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0u; };
-  constexpr int kRowGroups = moe::kW4Warps / moe::kW4ExpertSplit;
-  for (int ph = 0; ph < 2; ++ph) {
-    const int I = ph ? s.inter : (s.n_shared ? s.shared_inter : 64);
-    __nv_bfloat16* act = ph ? h->at<__nv_bfloat16>(h->L.a) : h->at<__nv_bfloat16>(h->L.a_s);
-    moe::W4Phase& u = up.ph[ph];
-    u.geom = w4_geom(s.hidden, group, zeros);
-    u.blocks = 2 * I / moe::kW4Rows;
-    u.items = ceil_div(u.blocks, kRowGroups);
-    u.items_inv = inverse(u.items);
-    u.up_off = (uint32_t)(I / 16) * u.geom.panel_bytes;
-    u.x = static_cast<const __nv_bfloat16*>(x);
-    u.x_cols = s.hidden;
-    u.out = act;
-    u.out_cols = I;
-    moe::W4Phase& d = down.ph[ph];
-    d.geom = w4_geom(I, group, zeros);
-    d.blocks = s.hidden / moe::kW4Rows;
-    d.items = ceil_div(d.blocks, kRowGroups);
-    d.items_inv = inverse(d.items);
-    d.x = act;
-    d.x_cols = I;
-    d.out = ph ? y : y_s;
-    d.out_cols = s.hidden;
-  }
-  // persistent grids: every resident CTA, but no more than there can be items
-  const int most_units = (batch * s.top_k < s.n_experts ? batch * s.top_k : s.n_experts) +
-                         batch * s.top_k / moe::kMaxUnitTokens;
-  auto grid_for = [&](const moe::W4ExpertArgs& g, int ctas) {
-    const long long items = (long long)g.n_su * g.ph[0].items + (long long)most_units * g.ph[1].items;
-    const long long cap = (long long)ctas * h->num_sms;
-    return (int)(items < cap ? items : cap);
+  // arguments of a projection's kernel whose items are `rows` weight rows
+  auto args = [&](bool is_down, int rows) {
+    moe::W4ExpertArgs g{};
+    g.batch = batch;
+    g.top_k = s.top_k;
+    g.assign_slot = plan->assign_slot;
+    g.assign_w = plan->assign_w;
+    g.status = h->at<int>(h->L.status);
+    g.wait_limit = (int)(h->spin_limit < (uint32_t)moe::kTcWaitLimit ? h->spin_limit : moe::kTcWaitLimit);
+    g.shared_w = static_cast<const uint8_t*>(is_down ? shared_w2 : shared_w13);
+    for (int ph = 0; ph < 2; ++ph) {
+      const int I = ph ? s.inter : (s.n_shared ? s.shared_inter : 64);
+      __nv_bfloat16* act = ph ? h->at<__nv_bfloat16>(h->L.a) : h->at<__nv_bfloat16>(h->L.a_s);
+      moe::W4Phase& p = g.ph[ph];
+      p.geom = w4_geom(is_down ? I : s.hidden, group, zeros);
+      p.blocks = is_down ? s.hidden / moe::kW4Rows : 2 * I / moe::kW4Rows;
+      p.items = ceil_div(is_down ? s.hidden : 2 * I, rows);
+      p.items_inv = inverse(p.items);
+      p.up_off = is_down ? 0u : (uint32_t)(I / 16) * p.geom.panel_bytes;
+      p.x = is_down ? act : static_cast<const __nv_bfloat16*>(x);
+      p.x_cols = is_down ? I : s.hidden;
+      p.out = is_down ? static_cast<void*>(ph ? y : y_s) : act;
+      p.out_cols = is_down ? s.hidden : I;
+    }
+    return g;
   };
-  const W4Pick ku = pick_w4<false>(batch, group, zeros), kd = pick_w4<true>(batch, group, zeros);
+  constexpr int kLightRows = moe::kW4Rows * (moe::kW4Warps / moe::kW4ExpertSplit);
+  const moe::W4Units all{&plan->n_active, plan->unit_expert, plan->unit_begin, plan->unit_count};
+  const moe::W4Units light{&split->n_light, split->light[0], split->light[1], split->light[2]};
+  const moe::W4Units heavy{&split->n_heavy, split->heavy[0], split->heavy[1], split->heavy[2]};
+  // persistent grids: every resident CTA, but no more than there can be items
+  const int assigned = batch * s.top_k, most = assigned < s.n_experts ? assigned : s.n_experts;
+  auto grid_for = [&](const moe::W4ExpertArgs& g, int units, int ctas) {
+    const long long items = (long long)g.n_su * g.ph[0].items + (long long)units * g.ph[1].items;
+    const long long cap = (long long)ctas * h->num_sms;
+    return (int)(items < 1 ? 1 : (items < cap ? items : cap));
+  };
+  auto project = [&](bool is_down, const ExpertTable& tab) -> cudaError_t {
+    cudaError_t err;
+    const W4Pick k = is_down ? pick_w4<true>(batch, group, zeros) : pick_w4<false>(batch, group, zeros);
+    moe::W4ExpertArgs g = args(is_down, kLightRows);
+    if (two) {
+      moe::W4ExpertArgs t = args(is_down, moe::kTcRows);
+      t.n_su = s.n_shared;
+      t.units = heavy;
+      const W4Kernel tk = is_down ? pick_w4_tc<true>(group, zeros) : pick_w4_tc<false>(group, zeros);
+      const int many = assigned / (moe::kW4LightTokens + 1);
+      err = launch(tk, grid_for(t, many < most ? many : most, 1), moe::kW4TcThreads, (size_t)moe::kTcSmem, sm, true, t, tab);
+      if (err != cudaSuccess) return err;
+      ++kernels;
+      g.units = light;
+      g.beside = 1;
+    } else {
+      g.n_su = s.n_shared;
+      g.units = all;
+    }
+    err = launch(k.kern, grid_for(g, most, k.ctas), moe::kW4Threads, k.smem, sm, true, g, tab);
+    if (err == cudaSuccess) ++kernels;
+    return err;
+  };
 
   if ((e = mark(0)) != cudaSuccess) return bail(e);
   const RouterArgs ra = router_args(h, x, router_w, topk_ids, topk_w, batch);
   e = launch(pick_router(s.n_experts), ra.G, router_threads_for(s.n_experts),
              moe::router_smem_bytes(batch, s.n_experts, h->router_chunk_rows), sm, true, ra);
   if (e != cudaSuccess) return bail(e);
+  ++kernels;
   if ((e = mark(1)) != cudaSuccess || (e = mark(4)) != cudaSuccess) return bail(e);
-  e = launch(ku.kern, grid_for(up, ku.ctas), moe::kW4Threads, ku.smem, sm, true, up, *h->tab13);
-  if (e != cudaSuccess) return bail(e);
-  e = launch(kd.kern, grid_for(down, kd.ctas), moe::kW4Threads, kd.smem, sm, true, down, *h->tab2);
-  if (e != cudaSuccess) return bail(e);
+  if (two) {
+    if ((e = launch(moe::w4_split_kernel, 1, 1024, 0, sm, true, plan, split)) != cudaSuccess) return bail(e);
+    ++kernels;
+  }
+  if ((e = project(false, *h->tab13)) != cudaSuccess) return bail(e);
+  if ((e = project(true, *h->tab2)) != cudaSuccess) return bail(e);
   if ((e = mark(2)) != cudaSuccess || (e = mark(5)) != cudaSuccess) return bail(e);
   const int cgrid = ceil_div(batch * s.hidden / 4, 256);
   const auto xb = static_cast<const __nv_bfloat16*>(x);
@@ -801,8 +838,9 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
           : launch(moe::w4_combine_kernel<false>, cgrid, 256, 0, sm, true, xb, (const float*)y, ys, out, batch,
                    (int)s.hidden, (int)s.top_k);
   if (e != cudaSuccess) return bail(e);
+  ++kernels;
   if ((e = mark(3)) != cudaSuccess) return bail(e);
-  return finish_forward(h, sm, 4, batch);
+  return finish_forward(h, sm, kernels, batch);
 }
 
 int check_forward_args(moe_decode_ctx* h, const void* x, const void* router_w, const void* const* w13,

@@ -6,7 +6,7 @@
 //   y[slot, n] = w_slot * sum_c a[slot, c] W2[c, n]
 //   out[t, n]  = bf16(x[t, n] + y[t k + 0, n] + ... + y[t k + k - 1, n] + y_shared[t, n])
 //
-// Two persistent kernels of one template: a CTA takes items (128 weight rows of
+// Up to 16 tokens of an expert: two persistent kernels of one template: a CTA takes items (128 weight rows of
 // one unit -- an expert and up to 32 of its tokens), the shared expert's first:
 // those need nothing from the router, so with programmatic dependent launch
 // they stream while it runs, and the wait for its plan comes with the first
@@ -20,6 +20,7 @@
 
 #include "moe_device.cuh"
 #include "w4_core.cuh"
+#include "w4_tc.cuh"
 
 namespace moe {
 
@@ -36,12 +37,25 @@ struct W4Phase {
   int out_cols;
 };
 
+// The units a kernel takes: the plan's, or a list of some of them.
+struct W4Units {
+  const int *n, *expert, *begin, *count;
+};
+
 struct W4ExpertArgs {
   W4Phase ph[2];  // 0: shared expert, 1: routed experts
   const uint8_t* shared_w;
-  int n_su;       // units of the shared expert: ceil(batch / 32), 0 without one
+  int n_su;       // units of the shared expert, 0 without one or where another kernel has it
   int batch, top_k;
-  const Plan* plan;
+  W4Units units;
+  const int* assign_slot;
+  const float* assign_w;
+  // Where both kernels of a projection run, w4_expert_tc_kernel comes first: it
+  // waits for what is before it and lets this kernel start beside it, which waits
+  // for it in the end (so that who waits for this one has waited for both).
+  int beside;
+  int* status;    // w4_expert_tc_kernel: status word and limit of its waits
+  int wait_limit;
 };
 
 // An item's unit: loaded one item before the lane's tokens are, which are
@@ -75,8 +89,8 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
   bool have_plan = false;
   auto read_plan = [&]() {
     if (have_plan) return;
-    cudaGridDependencySynchronize();
-    n_items = shared_items + __ldcg(&a.plan->n_active) * a.ph[1].items;
+    if (!a.beside) cudaGridDependencySynchronize();
+    n_items = shared_items + __ldcg(a.units.n) * a.ph[1].items;
     have_plan = true;
   };
   // the next grid may be put in place as this one's CTAs leave; it waits for
@@ -108,7 +122,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
     if (p_item < shared_items || p_item >= n_items) return;
     int ph, u, blk;
     place(p_item, ph, u, blk);
-    p_expert = __ldcg(&a.plan->unit_expert[u]);
+    p_expert = __ldcg(a.units.expert + u);
   };
   W4Stream st;
   st.valid = 0xfu;
@@ -161,8 +175,8 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
     int ph, u, blk;
     place(item, ph, u, blk);
     if (ph) {
-      un.begin = __ldcg(&a.plan->unit_begin[u]);
-      un.count = __ldcg(&a.plan->unit_count[u]);
+      un.begin = __ldcg(a.units.begin + u);
+      un.count = __ldcg(a.units.count + u);
     } else {
       un.begin = u * kMaxUnitTokens;
       un.count = min(kMaxUnitTokens, a.batch - un.begin);
@@ -175,7 +189,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int t = n * 8 + (lane >> 2), i = un.begin + (t < un.count ? t : 0);
-      slot[n] = routed ? __ldcg(&a.plan->assign_slot[i]) : i;
+      slot[n] = routed ? __ldcg(a.assign_slot + i) : i;
     }
   };
   auto rows_of = [&](const int (&slot)[NT], int ph, int s0, const T* (&xp)[NT]) {
@@ -217,8 +231,8 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
     W4Unit after;
     unit_of(item + 2 * step, after);
     if (warp == 0 && lane < un.count) {
-      s_row[parity][lane] = ph ? __ldcg(&a.plan->assign_slot[un.begin + lane]) : un.begin + lane;
-      if constexpr (DOWN) s_wt[parity][lane] = ph ? __ldcg(&a.plan->assign_w[un.begin + lane]) : 1.f;
+      s_row[parity][lane] = ph ? __ldcg(a.assign_slot + un.begin + lane) : un.begin + lane;
+      if constexpr (DOWN) s_wt[parity][lane] = ph ? __ldcg(a.assign_w + un.begin + lane) : 1.f;
     }
     float acc[kW4Panels][NT][4] = {};
     w4_run<T, C>(s0, s1, P.geom.tiles, ring, slot, xp, xr, n_tok_tiles, lane, acc, advance);
@@ -255,6 +269,168 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
     next = after;
     parity ^= 1;
   }
+  if (a.beside) cudaGridDependencySynchronize();
+}
+
+// ------------------------------------------------ experts of many tokens (tcgen05)
+// Above 16 tokens of a batch, experts that have more than 16 of them, and the
+// shared expert, go to w4_expert_tc_kernel with all their tokens at once; a
+// one-CTA kernel splits the plan's units (an expert's consecutive ones are joined).
+constexpr int kW4LightTokens = 16;
+struct W4Split {
+  int n_light, n_heavy, pad_[2];
+  int light[3][kMaxUnits];  // expert, begin, count
+  int heavy[3][kMaxExperts];
+};
+
+__global__ void __launch_bounds__(1024) w4_split_kernel(const Plan* plan, W4Split* out) {
+  __shared__ int s_warp[2][33];
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = plan->n_active;
+  int base[2] = {0, 0};  // light, heavy so far
+  for (int u0 = 0; u0 < n; u0 += 1024) {
+    const int u = u0 + tid;
+    int expert = -1, count = 0, kind = -1;
+    if (u < n) {
+      expert = plan->unit_expert[u];
+      if (u == 0 || plan->unit_expert[u - 1] != expert) {
+        for (int v = u; v < n && plan->unit_expert[v] == expert; ++v) count += plan->unit_count[v];
+        kind = count > kW4LightTokens;
+      }
+    }
+    unsigned m[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      m[k] = __ballot_sync(0xffffffffu, kind == k);
+      if (lane == 0) s_warp[k][warp] = __popc(m[k]);
+    }
+    __syncthreads();
+    if (warp < 2) {  // exclusive scan of the warps' numbers
+      const int v = s_warp[warp][lane];
+      int inc = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+      }
+      s_warp[warp][lane] = inc - v;
+      if (lane == 31) s_warp[warp][32] = inc;
+    }
+    __syncthreads();
+    if (kind >= 0) {
+      const int at = base[kind] + s_warp[kind][warp] + __popc(m[kind] & ((1u << lane) - 1u));
+      int* e = kind ? &out->heavy[0][at] : &out->light[0][at];
+      const int pitch = kind ? kMaxExperts : kMaxUnits;
+      e[0] = expert;
+      e[pitch] = plan->unit_begin[u];
+      e[2 * pitch] = count;
+    }
+    base[0] += s_warp[0][32];
+    base[1] += s_warp[1][32];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    out->n_light = base[0];
+    out->n_heavy = base[1];
+  }
+}
+
+// A CTA's items, 256 weight rows each: UP: 128 gate rows and their 128 up rows.
+template <bool DOWN>
+struct W4ExpertItems {
+  const W4ExpertArgs& a;
+  const ExpertTable& tab;
+  int idx, step, shared, total;  // the next item, ..., items of the shared expert, all items
+  int ph, blk, begin;            // the present one
+  __device__ bool next(W4TcItem& it) {
+    if (idx >= total) return false;
+    ph = idx >= shared;
+    const uint32_t i = idx - (ph ? shared : 0);
+    const W4Phase& P = a.ph[ph];
+    const int u = P.items_inv ? __umulhi(i, P.items_inv) : i;
+    blk = i - u * P.items;
+    idx += step;
+    const uint8_t* w;
+    if (ph) {
+      w = reinterpret_cast<const uint8_t*>(tab.p[__ldcg(a.units.expert + u)]);
+      begin = __ldcg(a.units.begin + u);
+      it.n_tok = __ldcg(a.units.count + u);
+    } else {
+      w = a.shared_w;
+      begin = 0;
+      it.n_tok = a.batch;
+    }
+    const int panels = P.out_cols / 16;  // of one projection
+    if constexpr (DOWN) {
+      it.panel[0] = w + (size_t)(16 * blk) * P.geom.panel_bytes;
+      it.panel[1] = it.panel[0] + (size_t)8 * P.geom.panel_bytes;
+      it.n_panels[0] = min(8, panels - 16 * blk);
+      it.n_panels[1] = max(0, min(8, panels - 16 * blk - 8));
+      if (it.n_panels[1] == 0) it.panel[1] = it.panel[0];
+    } else {
+      it.panel[0] = w + (size_t)(8 * blk) * P.geom.panel_bytes;
+      it.panel[1] = it.panel[0] + P.up_off;
+      it.n_panels[0] = it.n_panels[1] = min(8, panels - 8 * blk);
+    }
+    it.tile0 = 0;
+    it.tile1 = P.geom.tiles;
+    return true;
+  }
+  __device__ const W4Geom& geom() const { return a.ph[ph].geom; }
+  __device__ int slot(int t) const { return ph ? __ldcg(a.assign_slot + begin + t) : t; }
+  __device__ const __nv_bfloat16* rows() const { return a.ph[ph].x; }
+  __device__ uint32_t row(const W4TcItem&, int t) const {
+    const uint32_t s = (uint32_t)slot(t);
+    return ph && !DOWN ? s / (uint32_t)a.top_k : s;
+  }
+  __device__ long long offset(uint32_t row) const { return (long long)row * a.ph[ph].x_cols; }
+};
+
+template <int GROUP, bool ZP, bool DOWN>
+__global__ void __launch_bounds__(kW4TcThreads, 1)
+    w4_expert_tc_kernel(const __grid_constant__ W4ExpertArgs a, const __grid_constant__ ExpertTable tab) {
+  using T = __nv_bfloat16;
+  extern __shared__ __align__(1024) uint8_t w4_smem[];
+  __shared__ W4TcBars bars;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  w4_tc_begin(bars, a.wait_limit);
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int shared = a.n_su * a.ph[0].items;
+  W4ExpertItems<DOWN> items{a, tab, (int)blockIdx.x, (int)gridDim.x, shared,
+                            shared + __ldcg(a.units.n) * a.ph[1].items, 0, 0, 0};
+  if (warp < kTcUnpackers) {
+    w4_tc_unpack<T, GROUP, ZP>(w4_smem, bars, items, warp, a.status);
+  } else if (warp < kTcMmaWarp) {
+    const int f = warp - kTcUnpackers;
+    w4_tc_finish(bars, items, f, a.status,
+                 [&](const W4ExpertItems<DOWN>& now, const W4TcItem& it, int c, const float (&lo)[16], const float (&hi)[16]) {
+                   constexpr float unit = W4Dequant<T, ZP>::kUnit;
+                   const W4Phase& P = a.ph[now.ph];
+                   const int col = now.blk * (DOWN ? kTcRows : kTcRows / 2) + 32 * f + lane;
+#pragma unroll
+                   for (int n = 0; n < 16; ++n) {
+                     if (c + n < it.n_tok) {
+                       const size_t row = (size_t)now.slot(c + n) * P.out_cols;
+                       if constexpr (DOWN) {
+                         const float wt = unit * (now.ph ? __ldcg(a.assign_w + now.begin + c + n) : 1.f);
+                         float* y = static_cast<float*>(P.out) + row;
+                         if (col < P.out_cols) y[col] = wt * lo[n];
+                         if (col + 128 < P.out_cols) y[col + 128] = wt * hi[n];
+                       } else if (col < P.out_cols) {
+                         static_cast<T*>(P.out)[row + col] = __float2bfloat16_rn(silu_f32(unit * lo[n]) * (unit * hi[n]));
+                       }
+                     }
+                   }
+                 });
+  } else if (warp == kTcMmaWarp) {
+    w4_tc_mma<T>(w4_smem, bars, items, a.status);
+  } else {
+    w4_tc_stage<T>(w4_smem, bars, items, warp - kTcMmaWarp - 1, a.status);
+  }
+  w4_tc_end(bars);
 }
 
 // out[t, c] = bf16_rne(x[t, c] + sum_j y[t k + j, c] + y_shared[t, c]); PARTIAL:

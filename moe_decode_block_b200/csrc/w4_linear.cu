@@ -135,7 +135,8 @@ struct W4LinearItems {
   }
   __device__ const W4Geom& geom() const { return a.geom; }
   __device__ const T* rows() const { return static_cast<const T*>(a.x); }
-  __device__ long long row_offset(const W4TcItem&, int t) const { return t * a.x_stride; }
+  __device__ uint32_t row(const W4TcItem&, int t) const { return (uint32_t)t; }
+  __device__ long long offset(uint32_t row) const { return row * a.x_stride; }
 };
 
 template <typename T, int GROUP, bool ZP>
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
   } else if (warp < kTcMmaWarp) {
     const int row = (warp - kTcUnpackers) * 32 + lane;
     w4_tc_finish(bars, items, warp - kTcUnpackers, status,
-                 [&](const W4TcItem& it, int c, const float (&lo)[16], const float (&hi)[16]) {
+                 [&](const W4LinearItems<T>&, const W4TcItem& it, int c, const float (&lo)[16], const float (&hi)[16]) {
                    constexpr float unit = W4Dequant<T, ZP>::kUnit;
 #pragma unroll
                    for (int n = 0; n < 16; ++n) {

@@ -32,9 +32,8 @@
 //                 both accumulators);
 //   1 MMA warp    one thread issues a step's tcgen05.mma and commits;
 //   3 stagers     each every third step: the tokens' activations to shared memory
-//                 as the B operand, by asynchronous copies of 8 bytes (K-major
-//                 cores of 8 tokens x 8 inputs; 8-byte pieces move so that the
-//                 inputs' order is the A operand's).
+//                 as the B operand (K-major cores of 8 tokens x 8 inputs; 8-byte
+//                 pieces move so that the inputs' order is the A operand's).
 // Tensor memory: the sums (128 columns) and three buffers of operands.  Every wait is bounded: a wait that runs out sets the status word and
 // the CTA's abort flag, and the CTA leaves after its own copies and MMAs in
 // flight have ended.
@@ -159,7 +158,7 @@ __device__ __forceinline__ uint32_t tc5_idesc(int n) {
 // MMA warp's time).  A probe of the loop may suspend the warp for 20 us.  After
 // ctl[1] of them, or once the CTA's abort flag ctl[0] is up, the wait gives up
 // (status word, abort flag) and returns false.
-__device__ __noinline__ bool tc_wait_long(uint32_t bar, uint32_t parity, int* status, volatile int* ctl) {
+static __device__ __noinline__ bool tc_wait_long(uint32_t bar, uint32_t parity, int* status, volatile int* ctl) {
   bool ok = false;
   for (int i = 0; i < ctl[1]; ++i) {
     uint32_t done;
@@ -338,63 +337,64 @@ __device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, I
   __syncwarp();
 }
 
-// A stager warp (0..2): the B operands of every third step.  `items.rows()` +
-// `items.row_offset(item, token)` is a token's activation row.
+// A stager warp (0..2): the B operands of every third step.  `items.row(item,
+// token)` numbers a token's activation row, `items.rows() + items.offset(row)` is it.
 template <typename T, typename Items>
 __device__ __forceinline__ void w4_tc_stage(uint8_t* smem, W4TcBars& bars, Items items, int stager, int* status) {
   const int lane = threadIdx.x & 31;
+  constexpr int kIts = kTcStep / 32;  // 16-byte pieces of a token for each lane
+  constexpr int kBatch = 4;           // token groups whose loads are in flight together
   uint32_t ci = 0;  // step of the item's first
-  // the copies of this warp's last step are handed over once they have landed,
-  // while the next step's are under way
-  uint32_t last = 0;
-  bool pending = false;
-  auto hand_over = [&]() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.b_full[last]);
-  };
   W4TcItem it;
   while (items.next(it)) {
     const int groups = tc_columns(it.n_tok) / 8, steps = it.steps();
+    // rows of tokens 8 g + lane % 8 (the first token for those that do not exist)
+    uint32_t row[kTcTokens / 8];
+#pragma unroll
+    for (int g = 0; g < kTcTokens / 8; ++g) {
+      const int t = 8 * g + (lane & 7);
+      row[g] = items.row(it, t < it.n_tok ? t : 0);
+    }
     for (int s = (int)((stager + kTcStagers - ci % kTcStagers) % kTcStagers); s < steps; s += kTcStagers) {
       const uint32_t i = ci + (uint32_t)s, at = i % kTcSlots;
-      if (!tc_wait(&bars.b_empty[at], ((i / kTcSlots) & 1u) ^ 1u, status, bars.ctl)) {
-        cp_async_wait<0>();
-        return;
-      }
-      // lane: token 8 g + lane % 8 (the first token for those that do not exist),
-      // piece t = lane / 8 of 32 inputs, whose 8-byte halves q go to cores
-      // 2 (2 h + q) + t / 2
       const int tile = it.tile0 + 2 * s;
-      const T* first = items.rows() + (size_t)tile * kW4Tile + 8 * (lane >> 3);
-      uint32_t dst = smem_addr(smem + kTcB + at * kTcBSlot) + (lane & 7) * 16 + (lane >> 4) * 128 + ((lane >> 3) & 1) * 8;
       const bool both = tile + 1 < it.tile1;
-      for (int g = 0; g < groups; ++g, dst += kTcStep * 16) {
-        const int t = 8 * g + (lane & 7);
-        const T* p = first + items.row_offset(it, t < it.n_tok ? t : 0);
+      // lane: piece t = lane / 8 of 32 inputs of its tokens
+      const T* first = items.rows() + (size_t)tile * kW4Tile + 8 * (lane >> 3);
+      uint4 v[kBatch][kIts];
+      auto load = [&](int g0) {
 #pragma unroll
-        for (int q = 0; q < kTcStep / 32; ++q) {
-          if (q == kW4Tile / 32 && !both) break;
-          cp_async_8(dst + q * 512, p + 32 * q);
-          cp_async_8(dst + q * 512 + 256, p + 32 * q + 4);
+        for (int j = 0; j < kBatch; ++j) {
+          const T* p = first + items.offset(row[g0 + j]);
+#pragma unroll
+          for (int q = 0; q < kIts; ++q)
+            if (g0 + j < groups && (q < kIts / 2 || both)) v[j][q] = *reinterpret_cast<const uint4*>(p + 32 * q);
         }
+      };
+      load(0);
+      if (!tc_wait(&bars.b_empty[at], ((i / kTcSlots) & 1u) ^ 1u, status, bars.ctl)) return;
+      // the 8-byte halves q of a piece go to cores 2 (2 h + q) + t / 2
+      uint8_t* dst = smem + kTcB + at * kTcBSlot + (lane & 7) * 16 + (lane >> 4) * 128 + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int g0 = 0; g0 < kTcTokens / 8; g0 += kBatch, dst += kBatch * kTcStep * 16) {
+        if (g0 >= groups) break;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+          for (int q = 0; q < kIts; ++q)
+            if (g0 + j < groups && (q < kIts / 2 || both)) {
+              uint8_t* o = dst + j * (kTcStep * 16) + q * 512;
+              *reinterpret_cast<uint2*>(o) = make_uint2(v[j][q].x, v[j][q].y);
+              *reinterpret_cast<uint2*>(o + 256) = make_uint2(v[j][q].z, v[j][q].w);
+            }
+        if (g0 + kBatch < kTcTokens / 8 && g0 + kBatch < groups) load(g0 + kBatch);
       }
-      cp_async_commit();
-      if (pending) {
-        cp_async_wait<1>();
-        hand_over();
-      }
-      last = at;
-      pending = i >= kTcStagers;
-      if (!pending) {  // the first: the MMAs are waiting for it
-        cp_async_wait<0>();
-        hand_over();
-      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.b_full[at]);
     }
     ci += (uint32_t)steps;
   }
-  cp_async_wait<0>();
-  if (pending) hand_over();
 }
 
 // An unpacker warp (0..7): the A operands of two panels.
@@ -520,7 +520,7 @@ __device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Item
   cp_async_wait<0>();
 }
 
-// A finisher warp (0..3).  `take(item, c, lo, hi)` gets the sums of tokens c ..
+// A finisher warp (0..3).  `take(items, item, c, lo, hi)` gets the sums of tokens c ..
 // c + 15 of the lane's rows 32 finisher + lane of both accumulators; called for
 // every 16 tokens that there are.
 template <typename Items, typename Take>
@@ -536,7 +536,7 @@ __device__ __forceinline__ void w4_tc_finish(W4TcBars& bars, Items items, int fi
       float lo[16], hi[16];
       tc5_load16(d + c, lo);
       tc5_load16(d + 64u + c, hi);
-      take(it, c, lo, hi);
+      take(items, it, c, lo, hi);
     }
     tc5_fence_before();
     __syncwarp();

@@ -223,9 +223,10 @@ class W4Block:
 
         def add(rows, weight, w13, w2, inter):
             xr = xd[rows]
-            a13, a2 = dequant64(*w13), dequant64(*w2)
+            # above 16 tokens of the batch, an expert with more than 16 takes weights rounded to bf16
+            a13, a2 = _weights(*w13, len(xr)), _weights(*w2, len(xr))
             h = xr @ a13.T
-            dh = product_tolerance(H) * product_magnitude(xr, *w13)
+            dh = _fp32_error(xr, *w13, a13)
             g, u, dg, du = h[:, :inter], h[:, inter:], dh[:, :inter], dh[:, inter:]
             sig = torch.sigmoid(g)
             a = g * sig * u
@@ -233,7 +234,8 @@ class W4Block:
             da = 1.1 * dg * (u.abs() + du) + (g * sig).abs() * du + 2.0 ** -20 * a.abs()
             da = da + U[torch.bfloat16] * (a.abs() + da)  # stored in bf16
             y[rows] += weight * (a @ a2.T)
-            tol[rows] += weight * (da @ a2.abs().T + (product_tolerance(inter) + 2.0 ** -23) * product_magnitude(a.abs() + da, *w2))
+            most = a.abs() + da
+            tol[rows] += weight * (da @ a2.abs().T + _fp32_error(most, *w2, a2) + 2.0 ** -23 * product_magnitude(most, *w2))
 
         for e in torch.unique(ids).tolist():
             t, j = (ids == e).nonzero(as_tuple=True)
@@ -273,7 +275,7 @@ def test_block_every_element(shape, group, zeros, b):
         torch.cuda.synchronize()
         m.check(x, out, ids, w)
         assert blk.status() == MOE_OK
-        assert blk.stats()["last_kernels"] == 4
+        assert blk.stats()["last_kernels"] == (4 if b <= 16 else 7)
     finally:
         blk.close()
 
