@@ -409,6 +409,7 @@ int moe_decode_forward_w4(moe_decode_t h, const void* x, const void* router_w, c
 
 /* ---------------------------------------------------- the router's balance */
 #define MOE_BALANCE_MAX_TOKENS 16777216
+#define MOE_BALANCE_ONE_LAUNCH 512 /* tokens up to which one launch does everything */
 
 /* Workspace bytes of moe_balance_loss for n_experts (0 outside the envelope).
  * Host only. */
@@ -442,10 +443,12 @@ uint64_t moe_balance_workspace_bytes(int32_t n_experts);
  *   grad_loss   : device float32 [1], the loss's own gradient, or NULL (1)
  *   workspace   : device, moe_balance_workspace_bytes(n_experts) bytes,
  *                 16-byte aligned, of any content; two calls (or graphs) that
- *                 may run at the same time need one each
+ *                 may run at the same time need one each; NULL will do up to
+ *                 MOE_BALANCE_ONE_LAUNCH tokens
  * tokens 0..MOE_BALANCE_MAX_TOKENS; n_experts and top_k as moe_decode_shapes.
  * Loss sums in fp64 over rows of fp32; the same bits on every call.
- * Asynchronous on `stream` of the current device, one or two kernels.
+ * Asynchronous on `stream` of the current device: one kernel, or a memset and
+ * two.
  * Errors: MOE_ERR_UNSUPPORTED_SHAPE, MOE_ERR_INVALID_ARG, MOE_ERR_NO_DEVICE,
  * MOE_ERR_ARCH, MOE_ERR_CUDA.
  */

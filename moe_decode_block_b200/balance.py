@@ -10,6 +10,7 @@ from . import (MOE_DTYPE_BF16, MOE_DTYPE_FP16, MOE_DTYPE_FP32, _check, _current_
                _stream_handle, load_library)
 from .w4 import _on
 
+ONE_LAUNCH = 512  # tokens up to which no workspace is needed
 _TYPES = {}
 _WORKSPACE = {}
 
@@ -44,9 +45,9 @@ def balance_loss(logits, topk_ids, loss, counts, token_mask=None, router_bias=No
     then the live tokens) of logits [T, E] (float32, bfloat16 or float16; rows
     may be strided) and topk_ids [T, k] int32; with dlogits [T, E] also the
     gradient, times grad_loss [1].  token_mask [T] bool or uint8: 0 is a padded
-    token.  workspace: a uint8 tensor of workspace_bytes(E), by default a new
-    one (torch's allocator ties it to the current stream, so pass one when
-    `stream` is another)."""
+    token.  workspace (above ONE_LAUNCH tokens): a uint8 tensor of
+    workspace_bytes(E), by default a new one (torch's allocator ties it to the
+    current stream, so pass one when `stream` is another)."""
     T, E = logits.shape
     Ti, k = topk_ids.shape
     dev = logits.get_device()
@@ -54,13 +55,20 @@ def balance_loss(logits, topk_ids, loss, counts, token_mask=None, router_bias=No
     code = types.get(logits.dtype)
     zs = logits.stride()
     ds = (0, 1) if dlogits is None else dlogits.stride()
-    if (code is None or dev < 0 or Ti != T or (zs[1] != 1 and T) or (ds[1] != 1 and T) or topk_ids.dtype is not types["i32"]
-            or counts.dtype is not types["i32"] or loss.dtype is not types["f32"] or loss.numel() != 1
-            or counts.numel() != E + 1 or not topk_ids.is_contiguous() or not counts.is_contiguous()
-            or topk_ids.get_device() != dev or loss.get_device() != dev or counts.get_device() != dev
-            or token_mask is not None or router_bias is not None or dlogits is not None or workspace is not None):
+    i32, f32 = types["i32"], types["f32"]
+    if (code is None or dev < 0 or Ti != T or (zs[1] != 1 and T) or (ds[1] != 1 and T) or topk_ids.dtype is not i32
+            or counts.dtype is not i32 or loss.dtype is not f32 or loss.numel() != 1 or counts.numel() != E + 1
+            or not topk_ids.is_contiguous() or not counts.is_contiguous() or topk_ids.get_device() != dev
+            or loss.get_device() != dev or counts.get_device() != dev or token_mask is not None
+            or (router_bias is not None and (router_bias.dtype is not f32 or router_bias.numel() != E
+                                             or not router_bias.is_contiguous() or router_bias.get_device() != dev))
+            or (dlogits is not None and (dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape
+                                         or dlogits.get_device() != dev))
+            or (grad_loss is not None and (grad_loss.dtype is not f32 or grad_loss.numel() != 1
+                                           or grad_loss.get_device() != dev))
+            or workspace is not None):
         _look_closer(logits, topk_ids, loss, counts, token_mask, router_bias, dlogits, grad_loss, workspace)
-    if workspace is None:
+    if workspace is None and T > ONE_LAUNCH:
         if stream is not None and _stream_handle(stream) != _current_stream(dev):
             raise ValueError("workspace: needed with a stream that is not the current one")
         import torch
@@ -69,7 +77,7 @@ def balance_loss(logits, topk_ids, loss, counts, token_mask=None, router_bias=No
     args = (logits.data_ptr(), None if router_bias is None else router_bias.data_ptr(), topk_ids.data_ptr(),
             None if token_mask is None else token_mask.data_ptr(), loss.data_ptr(), counts.data_ptr(),
             None if dlogits is None else dlogits.data_ptr(), None if grad_loss is None else grad_loss.data_ptr(), T, E, k,
-            zs[0], ds[0], coef, code, workspace.data_ptr())
+            zs[0], ds[0], coef, code, None if workspace is None else workspace.data_ptr())
     if dev == _current_device():
         rc = call(*args, _current_stream(dev) if stream is None else _stream_handle(stream))
     else:

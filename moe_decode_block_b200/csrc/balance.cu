@@ -47,15 +47,12 @@ struct BalanceArgs {
   void* dlogits;          // or nullptr
   long long dstride;
   const float* grad_loss; // one float or nullptr (1)
-  int32_t* part;          // [n_part, E + 1] counts of the counting CTAs
-  int n_part;
   double* row_sums;       // [grid of the row kernel]
   unsigned* ticket;       // zeroed by the counting kernel
 };
 
 constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kBalCountCtas = 32;       // at most: every row CTA adds up their counts
 constexpr int kBalMaxCtas = 1024;       // row CTAs
 constexpr int kBalCluster = 8;          // CTAs of the one-launch kernel
 
@@ -86,7 +83,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_count_kernel(const __grid
   __syncthreads();
   balance_count(a, s_cnt, blockIdx.x, gridDim.x);
   __syncthreads();
-  for (int e = threadIdx.x; e <= a.E; e += kBalThreads) a.part[(size_t)blockIdx.x * (a.E + 1) + e] = s_cnt[e];
+  // (whole numbers: the order of the additions does not matter)
+  for (int e = threadIdx.x; e <= a.E; e += kBalThreads)
+    if (s_cnt[e]) atomicAdd(a.counts + e, s_cnt[e]);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
 }
 
@@ -121,6 +120,13 @@ __device__ __forceinline__ void store4(T* p, float4 v) {
     __stcs(reinterpret_cast<uint2*>(p),
            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)));
   }
+}
+
+// 2^x, flushing results below 2^-126 (two steps off at most)
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -160,15 +166,15 @@ struct BalanceRows {
     }
   }
   __device__ double run(int step, const float* s_c, float fg, int& n_rows) {
-    float c[CH][4], bias[CH][4];
+    float c[CH][4];
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = 4 * (lane + 32 * i) + j;
         c[i][j] = e < a.E ? s_c[e] : 0.f;
-        bias[i][j] = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
       }
+    constexpr float kLog2e = 1.4426950408889634f;
     double total = 0.0;
     n_rows = 0;
     while (r < a.tokens) {
@@ -177,11 +183,22 @@ struct BalanceRows {
       const int row = r;
       float m = -INFINITY;
       if (now) {
+        if (a.bias) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int e = 4 * (lane + 32 * i);
+            if (e < a.E) {
+              const float* b = a.bias + e;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) z[i][j] += __ldg(b + j);
+            }
+          }
+        }
 #pragma unroll
         for (int i = 0; i < CH; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            ex[i][j] = z[i][j] + bias[i][j];
+            ex[i][j] = z[i][j];
             m = fmaxf(m, ex[i][j]);
           }
       }
@@ -200,18 +217,28 @@ struct BalanceRows {
       }
       m = warp_max(m);
       const bool some = m != -INFINITY;  // (NaN counts as some)
-      // the difference before the product with log2(e): the type's lowest
-      // value times log2(e) would be -inf, and a row of it a NaN
-      const float top = some ? m : 0.f;
       float sum = 0.f, dot = 0.f;
+      auto take = [&](float& v, float arg, float cc) {
+        v = exp2_fast(arg);
+        sum += v;
+        dot = fmaf(v, cc, dot);
+      };
+      if (fabsf(m) < 0x1p+100f) {
+        // one rounding more of m log2(e), the same for the whole row: it drops out
+        const float ml = m * kLog2e;
 #pragma unroll
-      for (int i = 0; i < CH; ++i)
+        for (int i = 0; i < CH; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ex[i][j] = exp2f((ex[i][j] - top) * 1.4426950408889634f);
-          sum += ex[i][j];
-          dot = fmaf(ex[i][j], c[i][j], dot);
-        }
+          for (int j = 0; j < 4; ++j) take(ex[i][j], fmaf(ex[i][j], kLog2e, -ml), c[i][j]);
+      } else {
+        // the difference before the product with log2(e): the type's lowest
+        // value times log2(e) would be -inf, and a row of it a NaN
+        const float top = some ? m : 0.f;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) take(ex[i][j], (ex[i][j] - top) * kLog2e, c[i][j]);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -222,13 +249,13 @@ struct BalanceRows {
       total += (double)dot;
       n_rows += some;
       if (d) {
-        const float g = fg * inv;
+        const float g = fg * inv, gdot = g * dot;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
           const int e = 4 * (lane + 32 * i);
           if (e < a.E)
-            store4(d + e, make_float4(ex[i][0] * g * (c[i][0] - dot), ex[i][1] * g * (c[i][1] - dot),
-                                      ex[i][2] * g * (c[i][2] - dot), ex[i][3] * g * (c[i][3] - dot)));
+            store4(d + e, make_float4(ex[i][0] * fmaf(c[i][0], g, -gdot), ex[i][1] * fmaf(c[i][1], g, -gdot),
+                                      ex[i][2] * fmaf(c[i][2], g, -gdot), ex[i][3] * fmaf(c[i][3], g, -gdot)));
         }
       }
     }
@@ -261,13 +288,10 @@ __global__ void __launch_bounds__(kBalThreads, CH <= 4 ? 2 : 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   BalanceRows<T, CH> rows(a, blockIdx.x * kBalWarps + warp);
   cudaGridDependencySynchronize();
-  // all counts: the counting CTAs' parts
   for (int e = tid; e <= a.E; e += kBalThreads) {
-    int v = 0;
-    for (int b = 0; b < a.n_part; ++b) v += __ldcg(a.part + (size_t)b * (a.E + 1) + e);
+    const int v = __ldcg(a.counts + e);
     if (e == a.E) sh.live = v;
     reinterpret_cast<int*>(s_c)[e] = v;
-    if (blockIdx.x == 0) a.counts[e] = v;
   }
   __syncthreads();
   const int live = sh.live, c0 = balance_centre(a, live);
@@ -357,21 +381,22 @@ bool balance_shape_ok(int tokens, int E, int k) {
          k <= kMaxTopK && k <= E;
 }
 
-size_t part_bytes(int E) { return ((size_t)kBalCountCtas * (E + 1) * 4 + 255) / 256 * 256; }
-
 template <typename T, int CH>
 int launch_balance(BalanceArgs a, int num_sms, cudaStream_t st) {
   cudaError_t e;
-  if (a.tokens <= kBalCluster * kBalWarps * 4) {
+  static_assert(kBalCluster * kBalWarps * 4 == MOE_BALANCE_ONE_LAUNCH, "tokens of the one-launch kernel");
+  if (a.tokens <= MOE_BALANCE_ONE_LAUNCH) {
     int s = 1;
     while (s < kBalCluster && s * kBalWarps < a.tokens) s *= 2;
     e = host_launch(balance_small_kernel<T, CH>, dim3((unsigned)s), kBalThreads, (size_t)(2 * a.E + 4) * 4, st, s, false, a);
     return e == cudaSuccess ? MOE_OK : host_fail_cuda(e);
   }
+  if ((e = cudaMemsetAsync(a.counts, 0, (size_t)(a.E + 1) * 4, st)) != cudaSuccess) return host_fail_cuda(e);
+  // counting: four choices to a thread, up to one CTA to an SM
   const long long ids = (long long)a.tokens * a.k;
   const long long want = (ids + kBalThreads * 4 - 1) / (kBalThreads * 4);
-  a.n_part = (int)(want < kBalCountCtas ? want : kBalCountCtas);
-  e = host_launch(balance_count_kernel, dim3((unsigned)a.n_part), kBalThreads, (size_t)(a.E + 1) * 4, st, 1, false, a);
+  const int n_count = (int)(want < num_sms ? want : num_sms);
+  e = host_launch(balance_count_kernel, dim3((unsigned)n_count), kBalThreads, (size_t)(a.E + 1) * 4, st, 1, false, a);
   if (e != cudaSuccess) return host_fail_cuda(e);
   int grid = (a.tokens + kBalWarps - 1) / kBalWarps;
   const int cap = num_sms * (CH <= 4 ? 2 : 1);
@@ -398,7 +423,7 @@ extern "C" {
 
 uint64_t moe_balance_workspace_bytes(int32_t n_experts) {
   if (n_experts < 8 || n_experts > moe::kMaxExperts || n_experts % 8) return 0;
-  return moe::part_bytes(n_experts) + (size_t)moe::kBalMaxCtas * 8 + 256;
+  return (uint64_t)moe::kBalMaxCtas * 8 + 256;
 }
 
 int moe_balance_loss(const void* logits, const float* router_bias, const int32_t* topk_ids, const uint8_t* token_mask,
@@ -408,7 +433,7 @@ int moe_balance_loss(const void* logits, const float* router_bias, const int32_t
   using namespace moe;
   if (!balance_shape_ok(tokens, n_experts, top_k)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16 && dtype != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;
-  if (!loss || !counts || !workspace || (tokens > 0 && (!logits || !topk_ids))) return MOE_ERR_INVALID_ARG;
+  if (!loss || !counts || (!workspace && tokens > MOE_BALANCE_ONE_LAUNCH) || (tokens > 0 && (!logits || !topk_ids))) return MOE_ERR_INVALID_ARG;
   const uintptr_t vec = dtype == MOE_DTYPE_FP32 ? 16 : 8;  // four logits at a time
   if (!host_aligned(logits, vec) || !host_aligned(dlogits, vec) || !host_aligned(topk_ids, 4) || !host_aligned(loss, 4) ||
       !host_aligned(counts, 4) || !host_aligned(router_bias, 4) || !host_aligned(grad_loss, 4) ||
@@ -435,9 +460,8 @@ int moe_balance_loss(const void* logits, const float* router_bias, const int32_t
   a.dstride = dlogits_stride;
   a.grad_loss = grad_loss;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.part = reinterpret_cast<int32_t*>(ws);
-  a.row_sums = reinterpret_cast<double*>(ws + part_bytes(n_experts));
-  a.ticket = reinterpret_cast<unsigned*>(ws + part_bytes(n_experts) + (size_t)kBalMaxCtas * 8);
+  a.row_sums = reinterpret_cast<double*>(ws);
+  a.ticket = reinterpret_cast<unsigned*>(ws + (size_t)kBalMaxCtas * 8);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (dtype) {
     case MOE_DTYPE_FP32: return pick_balance<float>(a, sms, st);

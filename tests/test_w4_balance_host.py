@@ -98,7 +98,7 @@ def test_balance_refusals(lib, mem):
 
     for kw in (dict(e=12), dict(e=0), dict(e=1032), dict(k=0), dict(k=17), dict(e=64, k=33), dict(t=-1), dict(t=(1 << 24) + 1)):
         assert call(**kw) == SHAPE, kw
-    for kw in (dict(z=None), dict(ids=None), dict(loss=None), dict(counts=None), dict(ws=None), dict(z=mem + 4), dict(z=mem + 4, dt=0),
+    for kw in (dict(z=None), dict(ids=None), dict(loss=None), dict(counts=None), dict(ws=None, t=513), dict(z=mem + 4), dict(z=mem + 4, dt=0),
                dict(ids=mem + 2), dict(loss=mem + 2), dict(counts=mem + 1), dict(d=mem + 8), dict(g=mem + 2), dict(bias=mem + 1),
                dict(ws=mem + 8), dict(zs=15), dict(zs=18), dict(d=mem, ds=15), dict(d=mem, ds=18), dict(dt=3), dict(dt=-1)):
         assert call(**kw) == BAD, kw
