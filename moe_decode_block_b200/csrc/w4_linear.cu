@@ -68,6 +68,10 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
   }
 
   const uint32_t ring_addr = smem_addr(ring);
+  // launched while the kernel before it runs; nothing is read before that has
+  // ended (the weights neither: it may be the one that lays them out)
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   uint32_t p_slot = 0, slot = 0;
   auto produce = [&]() {
     if (st.left > 0) w4_stream_step<C, true>(st, ring_addr + p_slot, lane);
@@ -170,7 +174,9 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
     static_cast<T*>(a.out)[tok * a.out_stride + n] = W4Type<T>::from_f32(v);
   };
 
+  cudaTriggerProgrammaticLaunchCompletion();
   w4_tc_begin(bars, kTcWaitLimit);
+  cudaGridDependencySynchronize();
   int* status = &g_w4_linear_status;
   if (warp < kTcUnpackers) {
     w4_tc_unpack<T, GROUP, ZP>(w4_smem, bars, items, warp, status);
@@ -283,7 +289,7 @@ int launch_linear(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) 
   const int tok_blocks = (a.batch + NT * 8 - 1) / (NT * 8);
   const int s = cluster_for(row_blocks * tok_blocks, w4_steps(a.geom), C::kMinCtas * num_sms);
   const cudaError_t e =
-      host_launch(kern, dim3((unsigned)(row_blocks * s), (unsigned)tok_blocks), kW4Threads, C::kSmem, st, s, false, a);
+      host_launch(kern, dim3((unsigned)(row_blocks * s), (unsigned)tok_blocks), kW4Threads, C::kSmem, st, s, true, a);
   return e == cudaSuccess ? MOE_OK : host_fail_cuda(e);
 }
 
@@ -298,7 +304,7 @@ int launch_linear_tc(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t s
   int s = 1;
   while (s < 8 && 2 * s * row_blocks <= num_sms && a.geom.tiles >= 4 * s) s *= 2;
   const cudaError_t e =
-      host_launch(kern, dim3((unsigned)(row_blocks * s)), kW4TcThreads, kTcSmem, st, s, false, a);
+      host_launch(kern, dim3((unsigned)(row_blocks * s)), kW4TcThreads, kTcSmem, st, s, true, a);
   return e == cudaSuccess ? MOE_OK : host_fail_cuda(e);
 }
 
