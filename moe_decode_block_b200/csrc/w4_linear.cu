@@ -174,8 +174,10 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
     static_cast<T*>(a.out)[tok * a.out_stride + n] = W4Type<T>::from_f32(v);
   };
 
-  cudaTriggerProgrammaticLaunchCompletion();
+  // (tensor memory is held before the next kernel may come: one that takes tensor
+  // memory first and then waits for this grid would never end)
   w4_tc_begin(bars, kTcWaitLimit);
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   int* status = &g_w4_linear_status;
   if (warp < kTcUnpackers) {
