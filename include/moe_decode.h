@@ -142,7 +142,7 @@ extern "C" {
  * stay bf16.  Needs hidden, inter and shared_inter to be multiples of 64;
  * combinable with MOE_FLAG_PARTIAL_SUM only.  The handle's workspace grows by
  * max_batch * (top_k + n_shared) * hidden * 4 bytes (and 25 KB for more than
- * 16 tokens).
+ * 8 tokens).
  */
 #define MOE_FLAG_W4_WEIGHTS 64u
 typedef struct moe_decode_shapes {
@@ -386,14 +386,14 @@ int moe_w4_linear_status(void* stream);
 /*
  * moe_decode_forward with 4-bit expert weights (a handle created with
  * MOE_FLAG_W4_WEIGHTS).  x, router_w, out, topk_ids, topk_w and batch as for
- * moe_decode_forward; four kernels on `stream`, seven above 16 tokens.
+ * moe_decode_forward; four kernels on `stream`, seven above 8 tokens.
  *   w13 : HOST array of n_experts device pointers -> packed [2 * inter, hidden]
  *         (outputs [0, inter) the gate, [inter, 2 * inter) the up projection)
  *   w2  : HOST array of n_experts device pointers -> packed [hidden, inter]
  *   shared_w13, shared_w2 : device, packed (NULL iff n_shared == 0)
  *   group, has_zeros : of every matrix; scales (and zero points) in bf16
- * Products and sums in fp32.  Up to 16 tokens no weight is rounded; above, the
- * shared expert and the experts that more than 16 tokens chose take each
+ * Products and sums in fp32.  Up to 8 tokens no weight is rounded; above, the
+ * shared expert and the experts that more than 8 tokens chose take each
  * weight s (q - z) rounded once to bf16 (s below 2^27).  The experts' products
  * are added in a fixed order: the outputs are the same bits on every call with
  * the same routing weights.  Stage counters of

@@ -677,23 +677,18 @@ struct W4Pick {
   W4Kernel kern;
   int smem, ctas;  // dynamic shared memory, CTAs per SM
 };
-template <int NT, int GROUP, bool ZP, bool DOWN>
+template <int GROUP, bool ZP, bool DOWN>
 W4Pick w4_pick_of() {
-  using C = moe::W4Cfg<NT, GROUP, ZP, moe::kW4ExpertSplit>;
-  return {moe::w4_expert_kernel<NT, GROUP, ZP, DOWN>, C::kSmem, C::kMinCtas};
+  using C = moe::W4Cfg<1, GROUP, ZP, moe::kW4ExpertSplit>;
+  return {moe::w4_expert_kernel<GROUP, ZP, DOWN>, C::kSmem, C::kMinCtas};
 }
-template <int NT, bool DOWN>
-W4Pick pick_w4_nt(int group, bool zeros) {
-  switch (group) {
-    case 32: return zeros ? w4_pick_of<NT, 32, true, DOWN>() : w4_pick_of<NT, 32, false, DOWN>();
-    case 64: return zeros ? w4_pick_of<NT, 64, true, DOWN>() : w4_pick_of<NT, 64, false, DOWN>();
-    default: return zeros ? w4_pick_of<NT, 128, true, DOWN>() : w4_pick_of<NT, 128, false, DOWN>();
-  }
-}
-// The instance for the tokens that a unit of its own can have at this batch.
 template <bool DOWN>
-W4Pick pick_w4(int batch, int group, bool zeros) {
-  return batch <= 8 ? pick_w4_nt<1, DOWN>(group, zeros) : pick_w4_nt<2, DOWN>(group, zeros);
+W4Pick pick_w4(int group, bool zeros) {
+  switch (group) {
+    case 32: return zeros ? w4_pick_of<32, true, DOWN>() : w4_pick_of<32, false, DOWN>();
+    case 64: return zeros ? w4_pick_of<64, true, DOWN>() : w4_pick_of<64, false, DOWN>();
+    default: return zeros ? w4_pick_of<128, true, DOWN>() : w4_pick_of<128, false, DOWN>();
+  }
 }
 template <bool DOWN>
 W4Kernel pick_w4_tc(int group, bool zeros) {
@@ -708,11 +703,9 @@ int set_w4_attrs() {
   cudaError_t e;
   for (int group : {32, 64, 128})
     for (bool zeros : {false, true}) {
-      for (int batch : {8, 16}) {
-        const W4Pick up = pick_w4<false>(batch, group, zeros), down = pick_w4<true>(batch, group, zeros);
-        if ((e = raise_smem_limit(up.kern, up.smem)) != cudaSuccess) return fail_cuda(e);
-        if ((e = raise_smem_limit(down.kern, down.smem)) != cudaSuccess) return fail_cuda(e);
-      }
+      const W4Pick up = pick_w4<false>(group, zeros), down = pick_w4<true>(group, zeros);
+      if ((e = raise_smem_limit(up.kern, up.smem)) != cudaSuccess) return fail_cuda(e);
+      if ((e = raise_smem_limit(down.kern, down.smem)) != cudaSuccess) return fail_cuda(e);
       if ((e = raise_smem_limit(pick_w4_tc<false>(group, zeros), moe::kTcSmem)) != cudaSuccess) return fail_cuda(e);
       if ((e = raise_smem_limit(pick_w4_tc<true>(group, zeros), moe::kTcSmem)) != cudaSuccess) return fail_cuda(e);
     }
@@ -793,7 +786,7 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
   };
   auto project = [&](bool is_down, const ExpertTable& tab) -> cudaError_t {
     cudaError_t err;
-    const W4Pick k = is_down ? pick_w4<true>(batch, group, zeros) : pick_w4<false>(batch, group, zeros);
+    const W4Pick k = is_down ? pick_w4<true>(group, zeros) : pick_w4<false>(group, zeros);
     moe::W4ExpertArgs g = args(is_down, kLightRows);
     if (two) {
       moe::W4ExpertArgs t = args(is_down, moe::kTcRows);

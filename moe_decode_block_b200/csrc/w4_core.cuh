@@ -27,7 +27,8 @@
 // panel is one contiguous stream.  Word s of a lane holds step s of the tile:
 // bits 4j / 16 + 4j are output g + 8 (j & 1), inputs
 // 32 (s >> 1) + 8 t + 4 (s & 1) + 2 (j >> 1) and the next -- the order that
-// turns into the four A registers of m16n8k16 by masks, while the lane's B registers are 16 contiguous bytes of x.
+// turns into the four A registers of m16n8k16 by masks, while the lane's B
+// registers are 16 contiguous bytes of x.
 //
 // What bounds it.  HBM for large matrices up to 16 tokens, and not far behind it
 // the ALU pipe: 5 of its instructions for 8 codes, two cycles each, are 40 of
@@ -73,6 +74,7 @@ __host__ __device__ inline size_t w4_matrix_bytes(int n, int k, int group, bool 
 // by side in the outputs).
 template <int NT_, int GROUP, bool ZP_, int KS_>
 struct W4Cfg {
+  static_assert(NT_ == 1 || NT_ == 2, "token tiles");
   static constexpr int NT = NT_, KS = KS_;
   static constexpr bool ZP = ZP_;
   static constexpr int RW = kW4Warps / KS;              // row groups of 64 outputs
@@ -89,10 +91,9 @@ struct W4Cfg {
   // until the CTA has added them: 303 against 285 us for a full-size block of 8
   // tokens.)
   static constexpr int kSums = NT * 8 * kW4SumPitch * 4;
-  // two CTAs on an SM up to 16 tokens where two rings of two steps fit, one
-  // above (more accumulators)
+  // two CTAs on an SM where two rings of two steps fit
   static constexpr int fit(int kb) { return (kb * 1024 - 2048 - kW4Warps * kSums) / (kW4Warps * kSlot); }
-  static constexpr int kMinCtas = NT <= 2 && fit(114) >= 2 ? 2 : 1;
+  static constexpr int kMinCtas = fit(114) >= 2 ? 2 : 1;
   static constexpr int kFit = fit(kMinCtas == 2 ? 114 : 227);
   static constexpr int kDepth = kFit > 4 ? 4 : kFit;
   static constexpr int kRing = kW4Warps * kDepth * kSlot;
@@ -413,10 +414,8 @@ __device__ __forceinline__ void w4_run(int s0, int s1, int tiles, const uint8_t*
   } else {
     if (n_tok_tiles == 1)
       w4_run_tokens<T, C, 1>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
-    else if (C::NT == 2 || n_tok_tiles == 2)
-      w4_run_tokens<T, C, 2>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
     else
-      w4_run_tokens<T, C, C::NT>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
+      w4_run_tokens<T, C, 2>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
   }
 }
 

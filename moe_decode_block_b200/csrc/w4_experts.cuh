@@ -6,16 +6,29 @@
 //   y[slot, n] = w_slot * sum_c a[slot, c] W2[c, n]
 //   out[t, n]  = bf16(x[t, n] + y[t k + 0, n] + ... + y[t k + k - 1, n] + y_shared[t, n])
 //
-// Up to 16 tokens of an expert: two persistent kernels of one template: a CTA takes items (128 weight rows of
-// one unit -- an expert and up to 32 of its tokens), the shared expert's first:
-// those need nothing from the router, so with programmatic dependent launch
-// they stream while it runs, and the wait for its plan comes with the first
-// routed item.  A warp's weight ring runs ahead over item borders.  An item's
-// sums are added over the CTA's warps in a fixed order, and every (token,
-// expert) product keeps its own fp32 row until the combine adds the rows in
-// the order of the token's choices: no atomics, the same bits every time.
-// (The rows cost 4 H bytes per choice against an expert's 1.5 H I: a 1,000th
-// at I = 2048.)
+// Experts of up to 8 tokens (an mma.sync token tile): a persistent kernel for
+// each projection, one template.  A CTA takes items (128 weight rows of one
+// expert), the shared expert's first: those need nothing from the router, so
+// with programmatic dependent launch they stream while it runs, and the wait for
+// its plan comes with the first routed item.  A warp's weight ring runs ahead
+// over item borders.  An item's sums are added over the CTA's warps in a fixed
+// order, and every (token, expert) product keeps its own fp32 row until the
+// combine adds the rows in the order of the token's choices: no atomics, the same
+// bits every time.  (The rows cost 4 H bytes per choice against an expert's
+// 1.5 H I: a 1,000th at I = 2048.)
+//
+// Experts of more tokens, and the shared expert of a batch above 8: the tcgen05
+// kernel of the same two projections (w4_tc.cuh, items of 256 weight rows), beside
+// which the first kind runs.  With mma.sync up to 16 tokens (two token tiles, 128
+// registers and 220 to 450 bytes of spills) the full-size block took 626 us
+// instead of 519 at 16 tokens, the block of 16 experts 181 instead of 138.
+//
+// What bounds it.  The full-size block: HBM at 8 tokens (64 experts, zero points:
+// 283 us, 5 TB/s), the router's 15 us and the latency of short kernels at one
+// token (61 us).  16 experts at 64 tokens: 182 us, of which the router takes 34,
+// the up projection 85 and the down projection 55: steps of w4_tc.cuh, and a last
+// wave of items that fills the GPU in part (272 items of the up projection on 148
+// SMs, 476 of the down projection).
 #pragma once
 
 #include "moe_device.cuh"
@@ -66,12 +79,13 @@ struct W4Unit {
   int begin;  // shared: first token; routed: first assignment of the plan
 };
 
+constexpr int kW4LightTokens = 8;  // of an expert, at most, that stays with w4_expert_kernel
 constexpr int kW4ExpertSplit = 4;  // warps that split K; the CTA's other factor of 2 stands in the rows
 
-template <int NT, int GROUP, bool ZP, bool DOWN>
-__global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSplit>::kMinCtas)
+template <int GROUP, bool ZP, bool DOWN>
+__global__ void __launch_bounds__(kW4Threads, W4Cfg<1, GROUP, ZP, kW4ExpertSplit>::kMinCtas)
     w4_expert_kernel(const __grid_constant__ W4ExpertArgs a, const __grid_constant__ ExpertTable tab) {
-  using C = W4Cfg<NT, GROUP, ZP, kW4ExpertSplit>;
+  using C = W4Cfg<1, GROUP, ZP, kW4ExpertSplit>;
   using T = __nv_bfloat16;
   extern __shared__ __align__(1024) uint8_t w4_smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -80,8 +94,8 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
   const uint32_t ring_addr = smem_addr(ring);
   float* sums = reinterpret_cast<float*>(w4_smem + C::kRing);  // the warps' sums of an item
 
-  __shared__ int s_row[2][kMaxUnitTokens];    // output rows of an item's tokens (by item parity)
-  __shared__ float s_wt[2][kMaxUnitTokens];   // DOWN: their routing weights
+  __shared__ int s_row[2][kW4LightTokens];   // output rows of an item's tokens (by item parity)
+  __shared__ float s_wt[2][kW4LightTokens];  // DOWN: their routing weights
 
   const int shared_items = a.n_su * a.ph[0].items;
   const int step = gridDim.x;
@@ -178,42 +192,36 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
       un.begin = __ldcg(a.units.begin + u);
       un.count = __ldcg(a.units.count + u);
     } else {
-      un.begin = u * kMaxUnitTokens;
-      un.count = min(kMaxUnitTokens, a.batch - un.begin);
+      un.begin = 0;
+      un.count = a.batch;
     }
   };
-  // the lane's tokens: row of the activations (routed: the assignment's slot),
-  // the first token's for those that do not exist
-  auto slots_of = [&](const W4Unit& un, bool routed, int (&slot)[NT]) {
+  // the lane's token: row of the activations (routed: the assignment's slot), the
+  // first token's for one that does not exist
+  auto slot_of = [&](const W4Unit& un, bool routed, int& slot) {
     if (un.count == 0) return;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int t = n * 8 + (lane >> 2), i = un.begin + (t < un.count ? t : 0);
-      slot[n] = routed ? __ldcg(a.assign_slot + i) : i;
-    }
+    const int t = lane >> 2, i = un.begin + (t < un.count ? t : 0);
+    slot = routed ? __ldcg(a.assign_slot + i) : i;
   };
-  auto rows_of = [&](const int (&slot)[NT], int ph, int s0, const T* (&xp)[NT]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = ph && !DOWN ? (int)((unsigned)slot[n] / (unsigned)a.top_k) : slot[n];
-      xp[n] = a.ph[ph].x + (size_t)row * a.ph[ph].x_cols + s0 * (2 * kW4Tile) + 8 * (lane & 3);
-    }
+  auto row_of = [&](int slot, int ph, int s0, const T* (&xp)[1]) {
+    const int row = ph && !DOWN ? (int)((unsigned)slot / (unsigned)a.top_k) : slot;
+    xp[0] = a.ph[ph].x + (size_t)row * a.ph[ph].x_cols + s0 * (2 * kW4Tile) + 8 * (lane & 3);
   };
 
   if constexpr (DOWN) read_plan();  // the activations are complete
   W4Unit un, next;
-  int next_slot[NT];
+  int next_slot = 0;
   unit_of(blockIdx.x, un);
   unit_of(blockIdx.x + step, next);
   W4X<T, C> xr;
-  const T* xp[NT];
+  const T* xp[1];
   int parity = 0;
   if (un.count > 0) {
     const int ph = (int)blockIdx.x >= shared_items;
     int s0, s1;
     steps_of(ph, s0, s1);
-    slots_of(un, ph, next_slot);
-    rows_of(next_slot, ph, s0, xp);
+    slot_of(un, ph, next_slot);
+    row_of(next_slot, ph, s0, xp);
     if (s0 < s1) w4_first_x<T, C>(xp, 2 * s0 + 1 < a.ph[ph].geom.tiles, xr);
   }
   for (int item = blockIdx.x;; item += step) {
@@ -222,28 +230,27 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
     int ph, u, b0;  // b0: the item's first block
     place(item, ph, u, b0);
     const W4Phase& P = a.ph[ph];
-    const int n_tok_tiles = (un.count + 7) >> 3;
     int s0, s1;
     steps_of(ph, s0, s1);
     if (b0 + rg >= P.blocks) s1 = s0;  // no rows for this warp
     const int next_ph = item + step >= shared_items;
-    slots_of(next, next_ph, next_slot);
+    slot_of(next, next_ph, next_slot);
     W4Unit after;
     unit_of(item + 2 * step, after);
     if (warp == 0 && lane < un.count) {
       s_row[parity][lane] = ph ? __ldcg(a.assign_slot + un.begin + lane) : un.begin + lane;
       if constexpr (DOWN) s_wt[parity][lane] = ph ? __ldcg(a.assign_w + un.begin + lane) : 1.f;
     }
-    float acc[kW4Panels][NT][4] = {};
-    w4_run<T, C>(s0, s1, P.geom.tiles, ring, slot, xp, xr, n_tok_tiles, lane, acc, advance);
+    float acc[kW4Panels][1][4] = {};
+    w4_run<T, C>(s0, s1, P.geom.tiles, ring, slot, xp, xr, 1, lane, acc, advance);
     if (next.count > 0) {  // the next item's first activations, under this one's epilogue
       int n0, n1;
       steps_of(next_ph, n0, n1);
-      rows_of(next_slot, next_ph, n0, xp);
+      row_of(next_slot, next_ph, n0, xp);
       if (n0 < n1) w4_first_x<T, C>(xp, 2 * n0 + 1 < a.ph[next_ph].geom.tiles, xr);
     }
     __syncthreads();  // the last item's sums have been read
-    w4_store_sums<T, C>(sums + warp * (C::kSums / 4), lane, n_tok_tiles, acc);
+    w4_store_sums<T, C>(sums + warp * (C::kSums / 4), lane, 1, acc);
     __syncthreads();
 
     // thread: a row (of 128) of every second token; UP: a column (of 64) of every fourth
@@ -273,10 +280,9 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4ExpertSpli
 }
 
 // ------------------------------------------------ experts of many tokens (tcgen05)
-// Above 16 tokens of a batch, experts that have more than 16 of them, and the
+// Above 8 tokens of a batch, experts that have more than 8 of them, and the
 // shared expert, go to w4_expert_tc_kernel with all their tokens at once; a
 // one-CTA kernel splits the plan's units (an expert's consecutive ones are joined).
-constexpr int kW4LightTokens = 16;
 struct W4Split {
   int n_light, n_heavy, pad_[2];
   int light[3][kMaxUnits];  // expert, begin, count
@@ -405,7 +411,18 @@ __global__ void __launch_bounds__(kW4TcThreads, 1)
     w4_tc_unpack<T, GROUP, ZP>(w4_smem, bars, items, warp, a.status);
   } else if (warp < kTcMmaWarp) {
     const int f = warp - kTcUnpackers;
-    w4_tc_finish(bars, items, f, a.status,
+    // output rows (and routing weights) of tokens lane and lane + 32
+    int slot[kTcTokens / 32];
+    float wt[kTcTokens / 32];
+    const auto ready = [&](const W4ExpertItems<DOWN>& now, const W4TcItem& it) {
+#pragma unroll
+      for (int h = 0; h < kTcTokens / 32; ++h) {
+        const int t = 32 * h + lane;
+        slot[h] = t < it.n_tok ? now.slot(t) : 0;
+        if constexpr (DOWN) wt[h] = t < it.n_tok && now.ph ? __ldcg(a.assign_w + now.begin + t) : 1.f;
+      }
+    };
+    w4_tc_finish(bars, items, f, a.status, ready,
                  [&](const W4ExpertItems<DOWN>& now, const W4TcItem& it, int c, const float (&lo)[16], const float (&hi)[16]) {
                    constexpr float unit = W4Dequant<T, ZP>::kUnit;
                    const W4Phase& P = a.ph[now.ph];
@@ -413,12 +430,13 @@ __global__ void __launch_bounds__(kW4TcThreads, 1)
 #pragma unroll
                    for (int n = 0; n < 16; ++n) {
                      if (c + n < it.n_tok) {
-                       const size_t row = (size_t)now.slot(c + n) * P.out_cols;
+                       const int from = (c + n) & 31;
+                       const size_t row = (size_t)__shfl_sync(0xffffffffu, c < 32 ? slot[0] : slot[1], from) * P.out_cols;
                        if constexpr (DOWN) {
-                         const float wt = unit * (now.ph ? __ldcg(a.assign_w + now.begin + c + n) : 1.f);
+                         const float w = unit * __shfl_sync(0xffffffffu, c < 32 ? wt[0] : wt[1], from);
                          float* y = static_cast<float*>(P.out) + row;
-                         if (col < P.out_cols) y[col] = wt * lo[n];
-                         if (col + 128 < P.out_cols) y[col + 128] = wt * hi[n];
+                         if (col < P.out_cols) y[col] = w * lo[n];
+                         if (col + 128 < P.out_cols) y[col + 128] = w * hi[n];
                        } else if (col < P.out_cols) {
                          static_cast<T*>(P.out)[row + col] = __float2bfloat16_rn(silu_f32(unit * lo[n]) * (unit * hi[n]));
                        }
@@ -428,7 +446,7 @@ __global__ void __launch_bounds__(kW4TcThreads, 1)
   } else if (warp == kTcMmaWarp) {
     w4_tc_mma<T>(w4_smem, bars, items, a.status);
   } else {
-    w4_tc_stage<T>(w4_smem, bars, items, warp - kTcMmaWarp - 1, a.status);
+    w4_tc_stage<T, kTcStagers>(w4_smem, bars, items, warp - kTcMmaWarp - 1, a.status);
   }
   w4_tc_end(bars);
 }

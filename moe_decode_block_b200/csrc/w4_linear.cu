@@ -31,6 +31,12 @@ struct W4LinearArgs {
 // few outputs still fills the GPU.  The partial sums are added in a fixed
 // order: warps first, then the cluster's CTAs through distributed shared
 // memory.  Nothing is kept in global memory between calls.
+//
+// Measured (device time, weights from HBM): 4,096 x 7,168 at one token 6.3 us (2.4
+// TB/s), 7,168 x 2,048 at 8 tokens with zero points 5.3 us, 256 x 256 2.7 us -- the
+// latency of a launch, one trip to HBM and the cluster's exchange bounds them; a
+// call from Python costs the host 6.8 us.  16,384 x 7,168 at 16 tokens: 23 us, 2.6
+// TB/s, the tensor pipe (976 products a clock and SM).
 template <typename T, int NT, int GROUP, bool ZP>
 __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kMinCtas)
     w4_linear_kernel(const __grid_constant__ W4LinearArgs a) {
@@ -43,8 +49,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row_blk = blockIdx.x / S;
-  const int tok0 = blockIdx.y * NT * 8;
-  const int n_tok = min(NT * 8, a.batch - tok0);
+  const int n_tok = a.batch;
   const int n_tok_tiles = (n_tok + 7) / 8;
 
   const int q = rank * kW4Warps + warp, Q = S * kW4Warps;
@@ -64,7 +69,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int t = n * 8 + (lane >> 2);
-    xp[n] = static_cast<const T*>(a.x) + (tok0 + (t < n_tok ? t : 0)) * a.x_stride + s0 * (2 * kW4Tile) + 8 * (lane & 3);
+    xp[n] = static_cast<const T*>(a.x) + (t < n_tok ? t : 0) * a.x_stride + s0 * (2 * kW4Tile) + 8 * (lane & 3);
   }
 
   const uint32_t ring_addr = smem_addr(ring);
@@ -104,7 +109,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
     const int n = row0 + row;
     if (n >= a.n_out) return;
     if (a.bias) v += W4Type<T>::to_f32(static_cast<const T*>(a.bias)[n]);
-    static_cast<T*>(a.out)[(tok0 + tok) * a.out_stride + n] = W4Type<T>::from_f32(v);
+    static_cast<T*>(a.out)[tok * a.out_stride + n] = W4Type<T>::from_f32(v);
   };
   for (int i = tid; i < n_tok * kW4Rows; i += kW4Threads) {
     const int tok = i / kW4Rows, row = i % kW4Rows;
@@ -125,7 +130,9 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
 }
 
 // More than 16 tokens: 256 outputs x up to 64 tokens on tcgen05 (w4_tc.cuh); the
-// CTAs of a cluster split K as above.
+// CTAs of a cluster split K as above.  16,384 x 7,168 at 64 tokens: 27 us.  (With
+// the sums read by four warps, and each thread waiting for one remote value after
+// another, 31 us.)
 template <typename T>
 struct W4LinearItems {
   const W4LinearArgs& a;
@@ -143,6 +150,12 @@ struct W4LinearItems {
   __device__ long long offset(uint32_t row) const { return row * a.x_stride; }
 };
 
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(T lo, T hi) {
+  static_assert(sizeof(T) == 2, "16 bits");
+  return (uint32_t)*reinterpret_cast<const uint16_t*>(&lo) | (uint32_t)*reinterpret_cast<const uint16_t*>(&hi) << 16;
+}
+
 template <typename T, int GROUP, bool ZP>
 __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __grid_constant__ W4LinearArgs a) {
   extern __shared__ __align__(1024) uint8_t w4_smem[];
@@ -152,8 +165,8 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row0 = (int)(blockIdx.x / S) * kTcRows;
 
-  // K in pairs of tiles between the CTAs: each has some (cluster_for_tc)
-  const int pairs = (a.geom.tiles + 1) / 2;
+  // K in pairs of tiles between the CTAs: each has some (launch_linear_tc)
+  const int pairs = w4_steps(a.geom);
   W4LinearItems<T> items{a, {}, false};
   items.item.tile0 = 2 * (pairs * rank / S);
   items.item.tile1 = min(a.geom.tiles, 2 * (pairs * (rank + 1) / S));
@@ -167,12 +180,6 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
   // the rows' sums [token][row], over the B operands: the last MMAs have read them
   float* exch = reinterpret_cast<float*>(w4_smem + kTcB);
   static_assert(kTcSlots * kTcBSlot >= kTcTokens * kTcRows * 4, "rows' sums");
-  auto store = [&](int tok, int row, float v) {
-    const int n = row0 + row;
-    if (n >= a.n_out) return;
-    if (a.bias) v += W4Type<T>::to_f32(static_cast<const T*>(a.bias)[n]);
-    static_cast<T*>(a.out)[tok * a.out_stride + n] = W4Type<T>::from_f32(v);
-  };
 
   // (tensor memory is held before the next kernel may come: one that takes tensor
   // memory first and then waits for this grid would never end)
@@ -180,50 +187,80 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   int* status = &g_w4_linear_status;
-  if (warp < kTcUnpackers) {
+  // with one item the finishers have nothing to do until its end: they stage too
+  if (warp < kTcUnpackers)
     w4_tc_unpack<T, GROUP, ZP>(w4_smem, bars, items, warp, status);
-  } else if (warp < kTcMmaWarp) {
-    const int row = (warp - kTcUnpackers) * 32 + lane;
-    w4_tc_finish(bars, items, warp - kTcUnpackers, status,
-                 [&](const W4LinearItems<T>&, const W4TcItem& it, int c, const float (&lo)[16], const float (&hi)[16]) {
-                   constexpr float unit = W4Dequant<T, ZP>::kUnit;
-#pragma unroll
-                   for (int n = 0; n < 16; ++n) {
-                     if (c + n < it.n_tok) {
-                       if (S == 1) {
-                         store(c + n, row, unit * lo[n]);
-                         store(c + n, row + 128, unit * hi[n]);
-                       } else {
-                         exch[(c + n) * kTcRows + row] = unit * lo[n];
-                         exch[(c + n) * kTcRows + row + 128] = unit * hi[n];
-                       }
-                     }
-                   }
-                 });
-  } else if (warp == kTcMmaWarp) {
+  else if (warp == kTcMmaWarp)
     w4_tc_mma<T>(w4_smem, bars, items, status);
-  } else {
-    w4_tc_stage<T>(w4_smem, bars, items, warp - kTcMmaWarp - 1, status);
+  else if (warp - kTcUnpackers - (warp > kTcMmaWarp) < kTcSlots)
+    w4_tc_stage<T, kTcSlots>(w4_smem, bars, items, warp - kTcUnpackers - (warp > kTcMmaWarp), status);
+
+  // then every warp takes 16 tokens of its quarter of both accumulators' rows
+  static_assert(kW4TcThreads == 32 * 4 * (kTcTokens / 16), "a warp's quarter and tokens");
+  const int c = 16 * (warp >> 2);
+  if (c < a.batch && tc_wait(&bars.d_full[0], 0u, status, bars.ctl)) {
+    tc5_fence_after();
+    constexpr float unit = W4Dequant<T, ZP>::kUnit;
+    const uint32_t d = bars.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c;
+    float* to = exch + c * kTcRows + 32 * (warp & 3) + lane;
+    float lo[16], hi[16];
+    tc5_load16(d, lo);
+    tc5_load16(d + kTcTokens, hi);
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      if (c + n < a.batch) {
+        to[n * kTcRows] = unit * lo[n];
+        to[n * kTcRows + 128] = unit * hi[n];
+      }
+    }
   }
   w4_tc_end(bars);
-  if (S == 1) return;
+
+  // a thread: four rows of every (8 S)-th token, the CTAs' sums added in their order
+  const int row = tid % (kTcRows / 4) * 4, n = row0 + row;
+  const int step = S * (kW4TcThreads / (kTcRows / 4));
+  float bias[4] = {};
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.n_out) bias[i] = W4Type<T>::to_f32(static_cast<const T*>(a.bias)[n + i]);
+  }
+  // one 8-byte store where the four exist and their address allows it
+  const bool whole = n + 4 <= a.n_out && ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.out_stride * 2)) & 7) == 0;
   cluster.sync();
-  // four rows of a token at a time
-  for (int i = rank * kW4TcThreads + tid; i < a.batch * (kTcRows / 4); i += S * kW4TcThreads) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+  constexpr int kBatch = 4;  // tokens whose loads from the other CTAs are in flight together
+  for (int tok0 = (rank * kW4TcThreads + tid) / (kTcRows / 4); tok0 < a.batch; tok0 += kBatch * step) {
+    float v[kBatch][4] = {};
     for (int r = 0; r < S; ++r) {
-      const float4 p = reinterpret_cast<const float4*>(cluster.map_shared_rank(exch, r))[i];
-      v.x += p.x;
-      v.y += p.y;
-      v.z += p.z;
-      v.w += p.w;
+      const float* from = cluster.map_shared_rank(exch, r) + row;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (tok0 + u * step < a.batch) {
+          const float4 p = *reinterpret_cast<const float4*>(from + (tok0 + u * step) * kTcRows);
+          v[u][0] += p.x;
+          v[u][1] += p.y;
+          v[u][2] += p.z;
+          v[u][3] += p.w;
+        }
+      }
     }
-    const int tok = i / (kTcRows / 4), row = i % (kTcRows / 4) * 4;
-    store(tok, row, v.x);
-    store(tok, row + 1, v.y);
-    store(tok, row + 2, v.z);
-    store(tok, row + 3, v.w);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int tok = tok0 + u * step;
+      if (tok < a.batch) {
+        T* out = static_cast<T*>(a.out) + tok * a.out_stride + n;
+        T o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = W4Type<T>::from_f32(v[u][i] + bias[i]);
+        if (whole) {
+          *reinterpret_cast<uint2*>(out) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < a.n_out) out[i] = o[i];
+        }
+      }
+    }
   }
   cluster.sync();  // no CTA leaves while another reads its sums
 }
@@ -288,10 +325,8 @@ int launch_linear(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) 
   const int rc = host_raise_smem(kern, C::kSmem, dev, raised);
   if (rc != MOE_OK) return rc;
   const int row_blocks = (a.n_panels + kW4Panels - 1) / kW4Panels;
-  const int tok_blocks = (a.batch + NT * 8 - 1) / (NT * 8);
-  const int s = cluster_for(row_blocks * tok_blocks, w4_steps(a.geom), C::kMinCtas * num_sms);
-  const cudaError_t e =
-      host_launch(kern, dim3((unsigned)(row_blocks * s), (unsigned)tok_blocks), kW4Threads, C::kSmem, st, s, true, a);
+  const int s = cluster_for(row_blocks, w4_steps(a.geom), C::kMinCtas * num_sms);
+  const cudaError_t e = host_launch(kern, dim3((unsigned)(row_blocks * s)), kW4Threads, C::kSmem, st, s, true, a);
   return e == cudaSuccess ? MOE_OK : host_fail_cuda(e);
 }
 

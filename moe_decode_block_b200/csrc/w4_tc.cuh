@@ -1,21 +1,25 @@
-// w4_tc.cuh -- products of 17 to 64 tokens with a 4-bit weight matrix on the
-// 5th-generation tensor cores.
+// w4_tc.cuh -- products of many tokens (up to 64) with a 4-bit weight matrix on
+// the 5th-generation tensor cores: the dense layer above 16 tokens, the block's
+// experts above 8.
 //
 // mma.sync takes a token tile of 8 per instruction and does 1,024 products a
 // clock and SM whatever it is given (measured: 976), so at 64 tokens it stops at
 // 16 weights a clock and SM where HBM delivers 46.  tcgen05.mma takes all tokens
-// at once: 128 weight rows x up to 64 tokens x 16 inputs in 45 clocks (measured,
-// the same for 16, 32 and 64 tokens; the weights in tensor memory), 45 weights a
-// clock.
+// at once: 128 weight rows x up to 64 tokens x 16 inputs in 45 to 52 clocks
+// (measured, the same for 16, 32 and 64 tokens; the weights in tensor memory), 40
+// to 45 weights a clock.  A layer of 16,384 x 7,168 takes 23 us at 9 to 16 tokens
+// with mma.sync (two token tiles), 24.5 at 17 to 32 and 27 at 64 here: the dense
+// layer changes over above 16 tokens.  In the block, whose two-tile mma.sync
+// instance spilled, the change comes above 8 (w4_experts.cuh).
 //
 // Mathematics.  Here a weight s (q - z) is rounded once to the activations' type
 // (half a step: 2^-9 relative in bf16, 2^-12 in fp16; powers of two times s are
 // exact) and the products are summed in fp32 over all of K in tensor memory.  The
 // exact form of w4_core.cuh -- a group's sum read back and scaled in fp32 -- was
 // built too: reading 64 sums a row back every 128 inputs, beside the MMAs' own
-// traffic to tensor memory, took 1,700 clocks a step where the MMAs take 860,
-// 52 us for a layer of 16,384 x 7,168 at 64 tokens against MEASURED_US.  The
-// rounding adds 6e-4 to the 1.7e-3 that rounding the result to bf16 costs.
+// traffic to tensor memory, took 1,700 clocks a step where the MMAs take 860, 52
+// us for a layer of 16,384 x 7,168 at 64 tokens where the rounded form then took
+// 38.  The rounding adds 6e-4 to the 1.7e-3 that rounding the result to bf16 costs.
 //
 // A code becomes an operand by a mask (a subnormal, as in w4_core.cuh) and, in
 // bf16 without zero points, one fused multiply-add, q (s 2^100) - 8 s 2^-33, whose
@@ -29,14 +33,28 @@
 //                 copies and stores their operands to tensor memory with the
 //                 16x256b shape, whose fragment order is the packed layout's;
 //   4 finishers   read an item's sums out of tensor memory (a thread is a row of
-//                 both accumulators);
+//                 both accumulators) while the next item is multiplied;
 //   1 MMA warp    one thread issues a step's tcgen05.mma and commits;
 //   3 stagers     each every third step: the tokens' activations to shared memory
 //                 as the B operand (K-major cores of 8 tokens x 8 inputs; 8-byte
 //                 pieces move so that the inputs' order is the A operand's).
-// Tensor memory: the sums (128 columns) and three buffers of operands.  Every wait is bounded: a wait that runs out sets the status word and
-// the CTA's abort flag, and the CTA leaves after its own copies and MMAs in
-// flight have ended.
+// The dense layer's CTA has one item: its finishers stage too (six warps), and in
+// the end all 16 warps read the sums.  Tensor memory: two sets of sums (128
+// columns each) and two buffers of operands.  (One set and three buffers: 211
+// against 200 us for a block of 16 experts at 64 tokens.)
+//
+// What bounds it.  A step takes 1,130 clocks (0.6 us) at 17 to 64 tokens, of which
+// its 16 MMAs, each reading 128 rows of operands from tensor memory, are 720 to
+// 830; HBM gives 3.5 TB/s meanwhile.  Before, the load and store pipe was in the
+// way: a load of 16 bytes from each of 8 tokens x 4 touches 8 lines where 4 tokens
+// x 8 touch 4 (35 against 37 us for the layer above, 178 against 200 for the
+// block), and asynchronous 8-byte copies, straight to their places, twice as many
+// (48 us).  Around its 28 steps the layer above spends 9 us at 64 tokens: the
+// launch, first loads from HBM, and the exchange of the halves of K.
+//
+// Every wait is bounded: a wait that runs out sets the status word and the CTA's
+// abort flag, and the CTA leaves after its own copies and MMAs in flight have
+// ended.
 #pragma once
 
 #include "moe_device.cuh"
@@ -52,15 +70,19 @@ constexpr int kTcTokens = 64;
 constexpr int kTcStep = 128;     // inputs of a step
 constexpr int kTcRingTiles = 8;  // of an unpacker's ring: 2 panels x 512 bytes each
 constexpr int kTcRingBytes = kTcRingTiles * 2 * kW4TileBytes;
-constexpr int kTcSlots = 2 * kTcStagers;            // B operand slots: two for each stager
-constexpr int kTcBSlot = kTcTokens * kTcStep * 2;   // bytes
+constexpr int kTcSlots = 6;                           // of the B operands
+// Bytes between cores along K: 128, and a gap that puts the two cores which half a
+// warp writes (4 tokens x 4 pieces) on different banks.
+constexpr int kTcCore = 192;
+constexpr int kTcBGroup = kTcStep / 8 * kTcCore;      // of 8 tokens
+constexpr int kTcBSlot = kTcTokens / 8 * kTcBGroup;   // bytes
 constexpr int kTcB = kTcUnpackers * kTcRingBytes;   // offset of the B operands
 constexpr int kTcSmem = kTcB + kTcSlots * kTcBSlot;
-constexpr uint32_t kTcOperandCol = 128;             // first tensor-memory column of the A operands
-constexpr uint32_t kTcBufs = 3;                     // operand buffers
+constexpr uint32_t kTcOperandCol = 256;             // first tensor-memory column of the A operands
+constexpr uint32_t kTcBufs = 2;                     // operand buffers
 
 struct W4TcBars {
-  uint64_t a_full[kTcBufs], a_empty[kTcBufs], d_full, d_empty, b_full[kTcSlots], b_empty[kTcSlots], drained;
+  uint64_t a_full[kTcBufs], a_empty[kTcBufs], d_full[2], d_empty[2], b_full[kTcSlots], b_empty[kTcSlots], drained;
   uint32_t tmem;
   int ctl[2];  // abort flag, wait limit
 };
@@ -109,22 +131,15 @@ __device__ __forceinline__ void tc5_commit(uint64_t* bar, uint32_t lead) {
       "r"(lead)
       : "memory");
 }
-// Fragments of 8 columns each (output g: columns 2 t, 2 t + 1, then g + 8's) of
-// 16 lanes; N of them.
-template <int N>
-__device__ __forceinline__ void tc5_store_operands(uint32_t addr, const uint32_t (&r)[4 * N]) {
-  static_assert(N == 2 || N == 4, "fragments");
-  if constexpr (N == 4)
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-  else
-    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+// Four fragments of 8 columns each (output g: columns 2 t, 2 t + 1, then g + 8's)
+// of 16 lanes.
+__device__ __forceinline__ void tc5_store_operands(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 // 16 columns of this warp's 32 lanes (a thread is a lane); the wait that defines
 // them comes with the load.
@@ -186,10 +201,6 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* sta
 constexpr int kTcWaitLimit = 1 << 15;
 
 __device__ __forceinline__ int tc_columns(int n_tok) { return (n_tok + 15) / 16 * 16; }
-
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 
 // Codes as subnormals to weights.  `low` operands are outputs g's, the others
 // outputs (g + 8)'s, whose codes stand four bits higher.
@@ -258,8 +269,10 @@ __device__ __forceinline__ void w4_tc_begin(W4TcBars& bars, int limit) {
       mbar_init(&bars.a_full[i], kTcUnpackers);
       mbar_init(&bars.a_empty[i], 1);
     }
-    mbar_init(&bars.d_full, 1);
-    mbar_init(&bars.d_empty, kTcFinishers);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.d_full[i], 1);
+      mbar_init(&bars.d_empty[i], kTcFinishers);
+    }
     for (int i = 0; i < kTcSlots; ++i) {
       mbar_init(&bars.b_full[i], 1);
       mbar_init(&bars.b_empty[i], 1);
@@ -284,20 +297,19 @@ __device__ __forceinline__ void w4_tc_end(W4TcBars& bars) {
 
 // The MMA warp.  `items` gives the CTA's items in order: next(item) is false
 // after the last.  (Issued from a branch of one thread, whose operands have to be
-// moved to uniform registers one by one, a step's 16 took 1,030 clocks instead of
-// ISSUE_CLOCKS.)
+// moved to uniform registers one by one, a step's 16 took 1,030 clocks to issue.)
 template <typename T, typename Items>
 __device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, Items items, int* status) {
   const uint32_t lead = tc5_elect();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
-  const uint64_t b_first = tc5_desc(smem_addr(smem + kTcB), 128u, kTcStep * 16u);
+  const uint64_t b_first = tc5_desc(smem_addr(smem + kTcB), kTcCore, kTcBGroup);
   uint32_t buf = 0, buf_phase = 0, slot = 0, slot_phase = 0, item = 0;
   bool ok = true;
   W4TcItem it;
   for (; ok && items.next(it); ++item) {
     const uint32_t idesc = tc5_idesc<T>(tc_columns(it.n_tok));
-    const uint32_t d = tmem;
-    if (!(ok = tc_wait(&bars.d_empty, (item & 1u) ^ 1u, status, bars.ctl))) break;
+    const uint32_t d = tmem + 128u * (item & 1u);
+    if (!(ok = tc_wait(&bars.d_empty[item & 1u], ((item >> 1) & 1u) ^ 1u, status, bars.ctl))) break;
     for (int tile = it.tile0; tile < it.tile1; tile += 2) {
       ok = tc_wait(&bars.b_full[slot], slot_phase, status, bars.ctl) &&
            tc_wait(&bars.a_full[buf], buf_phase, status, bars.ctl);
@@ -308,14 +320,14 @@ __device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, I
       const uint32_t more = tile > it.tile0;
 #pragma unroll
       for (uint32_t k = 0; k < kW4Tile / 16; ++k) {
-        tc5_mma(d, a + 8u * k, b0 + 16u * k, idesc, k > 0 ? 1u : more, lead);
-        tc5_mma(d + 64u, a + 64u + 8u * k, b0 + 16u * k, idesc, k > 0 ? 1u : more, lead);
+        tc5_mma(d, a + 8u * k, b0 + (uint32_t)(kTcCore / 8) * k, idesc, k > 0 ? 1u : more, lead);
+        tc5_mma(d + 64u, a + 64u + 8u * k, b0 + (uint32_t)(kTcCore / 8) * k, idesc, k > 0 ? 1u : more, lead);
       }
       if (tile + 1 < it.tile1) {  // (the last step may be one tile)
 #pragma unroll
         for (uint32_t k = kW4Tile / 16; k < kTcStep / 16; ++k) {
-          tc5_mma(d, a + 8u * k, b0 + 16u * k, idesc, 1u, lead);
-          tc5_mma(d + 64u, a + 64u + 8u * k, b0 + 16u * k, idesc, 1u, lead);
+          tc5_mma(d, a + 8u * k, b0 + (uint32_t)(kTcCore / 8) * k, idesc, 1u, lead);
+          tc5_mma(d + 64u, a + 64u + 8u * k, b0 + (uint32_t)(kTcCore / 8) * k, idesc, 1u, lead);
         }
       }
       tc5_commit(&bars.a_empty[buf], lead);
@@ -329,7 +341,7 @@ __device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, I
         slot_phase ^= 1u;
       }
     }
-    tc5_commit(&bars.d_full, lead);
+    tc5_commit(&bars.d_full[item & 1u], lead);
   }
   // every MMA has ended before tensor memory goes back
   tc5_commit(&bars.drained, lead);
@@ -337,57 +349,62 @@ __device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, I
   __syncwarp();
 }
 
-// A stager warp (0..2): the B operands of every third step.  `items.row(item,
+// A stager warp (0 .. STAGERS - 1): the B operands of every STAGERS-th step.  `items.row(item,
 // token)` numbers a token's activation row, `items.rows() + items.offset(row)` is it.
-template <typename T, typename Items>
+template <typename T, int STAGERS, typename Items>
 __device__ __forceinline__ void w4_tc_stage(uint8_t* smem, W4TcBars& bars, Items items, int stager, int* status) {
+  // (a stager that was one step behind another's next use of its slot would take
+  // the phase before for the one it waits for)
+  static_assert(STAGERS <= kTcSlots, "a stager's step before step i + 2 kTcSlots has waited for step i's MMAs");
   const int lane = threadIdx.x & 31;
-  constexpr int kIts = kTcStep / 32;  // 16-byte pieces of a token for each lane
-  constexpr int kBatch = 4;           // token groups whose loads are in flight together
+  constexpr int kQuads = kTcTokens / 4;
+  constexpr int kBatch = kQuads / 2;  // fours of tokens whose loads are in flight together
+  // lane: token (lane / 4) % 4 of a four, 16 bytes (8 inputs) h, t of a tile's 8;
+  // their 8-byte halves q go to cores 2 (2 h + q) + t / 2
+  const int tok = (lane >> 2) & 3, h = lane >> 4, t = lane & 3;
+  uint8_t* to = smem + kTcB + tok * 16 + (4 * h + (t >> 1)) * kTcCore + (t & 1) * 8;
   uint32_t ci = 0;  // step of the item's first
   W4TcItem it;
   while (items.next(it)) {
-    const int groups = tc_columns(it.n_tok) / 8, steps = it.steps();
-    // rows of tokens 8 g + lane % 8 (the first token for those that do not exist)
-    uint32_t row[kTcTokens / 8];
+    const int quads = tc_columns(it.n_tok) / 4, steps = it.steps();
+    // rows of tokens 4 j + tok (the first token for those that do not exist)
+    uint32_t mine[kTcTokens / 32], row[kQuads];
 #pragma unroll
-    for (int g = 0; g < kTcTokens / 8; ++g) {
-      const int t = 8 * g + (lane & 7);
-      row[g] = items.row(it, t < it.n_tok ? t : 0);
-    }
-    for (int s = (int)((stager + kTcStagers - ci % kTcStagers) % kTcStagers); s < steps; s += kTcStagers) {
+    for (int k = 0; k < kTcTokens / 32; ++k) mine[k] = items.row(it, 32 * k + lane < it.n_tok ? 32 * k + lane : 0);
+#pragma unroll
+    for (int j = 0; j < kQuads; ++j) row[j] = __shfl_sync(0xffffffffu, mine[j / 8], (4 * j + tok) & 31);
+    for (int s = (int)((stager + STAGERS - ci % STAGERS) % STAGERS); s < steps; s += STAGERS) {
       const uint32_t i = ci + (uint32_t)s, at = i % kTcSlots;
       const int tile = it.tile0 + 2 * s;
       const bool both = tile + 1 < it.tile1;
-      // lane: piece t = lane / 8 of 32 inputs of its tokens
-      const T* first = items.rows() + (size_t)tile * kW4Tile + 8 * (lane >> 3);
-      uint4 v[kBatch][kIts];
-      auto load = [&](int g0) {
+      const T* first = items.rows() + (size_t)tile * kW4Tile + 32 * h + 8 * t;
+      uint4 v[kBatch][2];
+      auto load = [&](int j0) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          const T* p = first + items.offset(row[g0 + j]);
-#pragma unroll
-          for (int q = 0; q < kIts; ++q)
-            if (g0 + j < groups && (q < kIts / 2 || both)) v[j][q] = *reinterpret_cast<const uint4*>(p + 32 * q);
+          if (j0 + j < quads) {
+            const T* p = first + items.offset(row[j0 + j]);
+            v[j][0] = *reinterpret_cast<const uint4*>(p);
+            if (both) v[j][1] = *reinterpret_cast<const uint4*>(p + kW4Tile);
+          }
         }
       };
       load(0);
       if (!tc_wait(&bars.b_empty[at], ((i / kTcSlots) & 1u) ^ 1u, status, bars.ctl)) return;
-      // the 8-byte halves q of a piece go to cores 2 (2 h + q) + t / 2
-      uint8_t* dst = smem + kTcB + at * kTcBSlot + (lane & 7) * 16 + (lane >> 4) * 128 + ((lane >> 3) & 1) * 8;
+      uint8_t* dst = to + at * kTcBSlot;
 #pragma unroll
-      for (int g0 = 0; g0 < kTcTokens / 8; g0 += kBatch, dst += kBatch * kTcStep * 16) {
-        if (g0 >= groups) break;
+      for (int j0 = 0; j0 < kQuads; j0 += kBatch) {
+        if (j0 >= quads) break;
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
 #pragma unroll
-          for (int q = 0; q < kIts; ++q)
-            if (g0 + j < groups && (q < kIts / 2 || both)) {
-              uint8_t* o = dst + j * (kTcStep * 16) + q * 512;
-              *reinterpret_cast<uint2*>(o) = make_uint2(v[j][q].x, v[j][q].y);
-              *reinterpret_cast<uint2*>(o + 256) = make_uint2(v[j][q].z, v[j][q].w);
+          for (int tl = 0; tl < 2; ++tl)
+            if (j0 + j < quads && (tl == 0 || both)) {
+              uint8_t* o = dst + ((j0 + j) >> 1) * kTcBGroup + ((j0 + j) & 1) * 64 + tl * (8 * kTcCore);
+              *reinterpret_cast<uint2*>(o) = make_uint2(v[j][tl].x, v[j][tl].y);
+              *reinterpret_cast<uint2*>(o + 2 * kTcCore) = make_uint2(v[j][tl].z, v[j][tl].w);
             }
-        if (g0 + kBatch < kTcTokens / 8 && g0 + kBatch < groups) load(g0 + kBatch);
+        if (j0 + kBatch < kQuads && j0 + kBatch < quads) load(j0 + kBatch);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -479,7 +496,7 @@ __device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Item
 #pragma unroll
         for (int e = 0; e < kEntries; ++e) dq[p][e].set(e_next[p][e][0], e_next[p][e][1]);
       ask(tile + 2);
-      // the MMAs of three steps ago have read this buffer
+      // the MMAs of two steps ago have read this buffer
       if (!(ok = tc_wait(&bars.a_empty[buf], buf_phase ^ 1u, status, bars.ctl))) break;
       tc5_fence_after();
       const uint32_t a = a0 + buf * 128u;
@@ -503,7 +520,7 @@ __device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Item
             r[4 * i + 2] = q(o[1], 1);
             r[4 * i + 3] = q(o[3], 1);
           }
-          tc5_store_operands<4>(a + ((uint32_t)(16 * p) << 16) + 32u * ti, r);
+          tc5_store_operands(a + ((uint32_t)(16 * p) << 16) + 32u * ti, r);
         }
         slot = (slot + 2 * kW4TileBytes) % kTcRingBytes;
       }
@@ -522,16 +539,19 @@ __device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Item
 
 // A finisher warp (0..3).  `take(items, item, c, lo, hi)` gets the sums of tokens c ..
 // c + 15 of the lane's rows 32 finisher + lane of both accumulators; called for
-// every 16 tokens that there are.
-template <typename Items, typename Take>
-__device__ __forceinline__ void w4_tc_finish(W4TcBars& bars, Items items, int finisher, int* status, Take take) {
+// every 16 tokens that there are.  `ready(items, item)` comes before, while the
+// item is being multiplied.
+template <typename Items, typename Ready, typename Take>
+__device__ __forceinline__ void w4_tc_finish(W4TcBars& bars, Items items, int finisher, int* status, Ready ready,
+                                             Take take) {
   const uint32_t lanes = (uint32_t)(32 * finisher) << 16;
   uint32_t item = 0;
   W4TcItem it;
   for (; items.next(it); ++item) {
-    if (!tc_wait(&bars.d_full, item & 1u, status, bars.ctl)) return;
+    ready(items, it);
+    if (!tc_wait(&bars.d_full[item & 1u], (item >> 1) & 1u, status, bars.ctl)) return;
     tc5_fence_after();
-    const uint32_t d = bars.tmem + lanes;
+    const uint32_t d = bars.tmem + lanes + 128u * (item & 1u);
     for (int c = 0; c < it.n_tok; c += 16) {
       float lo[16], hi[16];
       tc5_load16(d + c, lo);
@@ -540,7 +560,7 @@ __device__ __forceinline__ void w4_tc_finish(W4TcBars& bars, Items items, int fi
     }
     tc5_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.d_empty);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.d_empty[item & 1u]);
   }
 }
 

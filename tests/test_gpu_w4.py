@@ -23,15 +23,15 @@ def _x(b, k, dtype, seed):
     return torch.randn(b, k, device="cuda", generator=g).to(dtype)
 
 
-def _weights(codes, scales, zeros, tokens):
-    """The weights as the products take them: exact up to 16 tokens, above rounded once to the scales' type."""
+def _weights(codes, scales, zeros, tokens, exact=16):
+    """The weights as the products take them: exact up to `exact` tokens, above rounded once to the scales' type."""
     w = dequant64(codes, scales, zeros)
-    return w if tokens <= 16 else w.to(scales.dtype).double()  # (12 to 15 bits: exact in the fp32 between)
+    return w if tokens <= exact else w.to(scales.dtype).double()  # (12 to 15 bits: exact in the fp32 between)
 
 
-def _fp32_error(x, codes, scales, zeros, w):
+def _fp32_error(x, codes, scales, zeros, w, exact=16):
     """What the fp32 sums may be off by, in 64 bits."""
-    if len(x) <= 16:
+    if len(x) <= exact:
         return product_tolerance(x.shape[1], x.dtype) * product_magnitude(x, codes, scales, zeros)
     # one chain of K / 16 instructions (each under 2^-23 of the sum of magnitudes), 8 CTAs, bias
     return (x.shape[1] / 16 + 10) * 2.0 ** -23 * (x.double().abs() @ w.abs().T)
@@ -223,10 +223,10 @@ class W4Block:
 
         def add(rows, weight, w13, w2, inter):
             xr = xd[rows]
-            # above 16 tokens of the batch, an expert with more than 16 takes weights rounded to bf16
-            a13, a2 = _weights(*w13, len(xr)), _weights(*w2, len(xr))
+            # an expert with more than 8 tokens takes weights rounded to bf16
+            a13, a2 = _weights(*w13, len(xr), exact=8), _weights(*w2, len(xr), exact=8)
             h = xr @ a13.T
-            dh = _fp32_error(xr, *w13, a13)
+            dh = _fp32_error(xr, *w13, a13, exact=8)
             g, u, dg, du = h[:, :inter], h[:, inter:], dh[:, :inter], dh[:, inter:]
             sig = torch.sigmoid(g)
             a = g * sig * u
@@ -235,7 +235,7 @@ class W4Block:
             da = da + U[torch.bfloat16] * (a.abs() + da)  # stored in bf16
             y[rows] += weight * (a @ a2.T)
             most = a.abs() + da
-            tol[rows] += weight * (da @ a2.abs().T + _fp32_error(most, *w2, a2) + 2.0 ** -23 * product_magnitude(most, *w2))
+            tol[rows] += weight * (da @ a2.abs().T + _fp32_error(most, *w2, a2, exact=8) + 2.0 ** -23 * product_magnitude(most, *w2))
 
         for e in torch.unique(ids).tolist():
             t, j = (ids == e).nonzero(as_tuple=True)
@@ -275,7 +275,7 @@ def test_block_every_element(shape, group, zeros, b):
         torch.cuda.synchronize()
         m.check(x, out, ids, w)
         assert blk.status() == MOE_OK
-        assert blk.stats()["last_kernels"] == (4 if b <= 16 else 7)
+        assert blk.stats()["last_kernels"] == (4 if b <= 8 else 7)
     finally:
         blk.close()
 
