@@ -10,7 +10,8 @@ import pytest
 import torch
 
 import oracle
-from moe_decode_block_b200 import MOE_OK, MoEDecode, MoEDecodeError, reduce_residual, router_topk_noalloc, synth, w4
+from moe_decode_block_b200 import (MOE_ERR_DEVICE_TIMEOUT, MOE_OK, MoEDecode, MoEDecodeError, reduce_residual,
+                                   router_topk_noalloc, synth, w4)
 from gpu_helpers import W_ATOL, margin_x
 from w4_reference import TINY as TINY_STEP
 from w4_reference import U, assert_within, dequant64, product_magnitude, product_tolerance, random_w4
@@ -188,6 +189,58 @@ def test_linear_same_bits_graph_streams_and_empty_batch():
     w4.linear(x[:0], packed, first[:0], 128, zeros=True)  # nothing to do
 
 
+@pytest.mark.parametrize("b,n,k", [(17, 256, 64), (64, 1536, 2048), (40, 300, 7168)])
+def test_linear_many_tokens_two_streams_two_graphs_and_status(b, n, k):
+    """Above 16 tokens: calls that overlap, on streams and in graphs, give the bits of one alone; no wait gives up."""
+    codes, scales, z = random_w4(n, k, 64, True, torch.float16, seed=25)
+    packed = w4.pack(codes, scales, z)
+    x = _x(b, k, torch.float16, seed=26)
+    first = torch.empty(b, n, dtype=torch.float16, device="cuda")
+    w4.linear(x, packed, first, 64, zeros=True)
+    assert w4.linear_status() == MOE_OK
+    _check_linear(x, codes, scales, z, None, first)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [torch.full_like(first, float("nan")) for _ in range(10)]
+    for i, o in enumerate(outs):
+        w4.linear(x, packed, o, 64, zeros=True, stream=side[i % 2])
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, first)
+        o.fill_(float("nan"))
+    graphs = []
+    for i in range(2):  # calls one behind the other, each started while the one before it ends
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            for o in outs[5 * i:5 * i + 5]:
+                w4.linear(x, packed, o, 64, zeros=True)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, st in zip(graphs, side):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, first)
+    assert w4.linear_status() == MOE_OK
+
+
+def test_linear_many_tokens_rows_apart_at_odd_addresses():
+    """Above 16 tokens: rows that start at any 16-bit element; what lies between them stays."""
+    b, n, k = 33, 261, 448
+    codes, scales, z = random_w4(n, k, 32, False, torch.bfloat16, seed=27)
+    packed = w4.pack(codes, scales, z)
+    x = _x(b, k, torch.bfloat16, seed=28)
+    bias = _x(1, n, torch.bfloat16, seed=29)[0]
+    for pitch, off in ((n, 0), (n + 3, 1), (n + 7, 4), (n + 7, 2)):  # the third: rows on 8-byte boundaries
+        buf = torch.full((b * pitch + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = buf[off:off + b * pitch].view(b, pitch)[:, :n]
+        w4.linear(x, packed, out, 32, bias=bias)
+        torch.cuda.synchronize()
+        _check_linear(x, codes, scales, z, bias, out.contiguous())
+        out.fill_(7.0)
+        assert bool((buf == 7.0).all())
+
+
 # ------------------------------------------------------------------ the block
 class W4Block:
     """Plain and packed weights of one block."""
@@ -306,6 +359,30 @@ def test_block_full_size_experts():
             out, ids, w = m.forward(blk, x)
             torch.cuda.synchronize()
             m.check(x, out, ids, w)
+    finally:
+        blk.close()
+        del m
+        torch.cuda.empty_cache()
+
+
+def test_block_short_wait_limit_is_reported_and_the_handle_recovers():
+    """One probe for each wait: a forward either ends in time and is right, or says that it did not."""
+    m = W4Block(synth.PROF, 128, False, seed=41)
+    blk = m.handle(40)
+    try:
+        x = margin_x(40, synth.PROF.hidden, m, synth.PROF.top_k, seed=445)
+        blk.set_wait_limit(1)
+        out, ids, w = m.forward(blk, x)
+        torch.cuda.synchronize()
+        st = blk.status()
+        assert st in (MOE_OK, MOE_ERR_DEVICE_TIMEOUT)
+        if st == MOE_OK:
+            m.check(x, out, ids, w)
+        blk.set_wait_limit(0)
+        out, ids, w = m.forward(blk, x)
+        torch.cuda.synchronize()
+        assert blk.status() == MOE_OK
+        m.check(x, out, ids, w)
     finally:
         blk.close()
         del m
