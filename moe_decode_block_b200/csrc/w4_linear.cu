@@ -3,6 +3,7 @@
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "moe_host.h"
 #include "w4_core.cuh"
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
 // More than 16 tokens: 256 outputs x up to 64 tokens on tcgen05 (w4_tc.cuh); the
 // CTAs of a cluster split K as above.  16,384 x 7,168 at 64 tokens: 27 us.  (With
 // the sums read by four warps, and each thread waiting for one remote value after
-// another, 31 us.)
+// another, 31 us.)  4,096 x 7,168 at 32 tokens: 14.7 us.
 template <typename T>
 struct W4LinearItems {
   const W4LinearArgs& a;
@@ -228,39 +229,51 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
   // one 8-byte store where the four exist and their address allows it
   const bool whole = n + 4 <= a.n_out && ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.out_stride * 2)) & 7) == 0;
   cluster.sync();
-  constexpr int kBatch = 4;  // tokens whose loads from the other CTAs are in flight together
-  for (int tok0 = (rank * kW4TcThreads + tid) / (kTcRows / 4); tok0 < a.batch; tok0 += kBatch * step) {
-    float v[kBatch][4] = {};
-    for (int r = 0; r < S; ++r) {
-      const float* from = cluster.map_shared_rank(exch, r) + row;
+  auto add = [&](auto splits) {
+    constexpr int N = decltype(splits)::value;  // S
+    constexpr int kBatch = 8 / N;               // tokens whose 8 loads from the CTAs are in flight together
+    const float* from[N];
+#pragma unroll
+    for (int r = 0; r < N; ++r) from[r] = cluster.map_shared_rank(exch, r) + row;
+    for (int tok0 = (rank * kW4TcThreads + tid) / (kTcRows / 4); tok0 < a.batch; tok0 += kBatch * step) {
+      float4 p[kBatch][N];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+          if (tok0 + u * step < a.batch) p[u][r] = *reinterpret_cast<const float4*>(from[r] + (tok0 + u * step) * kTcRows);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        if (tok0 + u * step < a.batch) {
-          const float4 p = *reinterpret_cast<const float4*>(from + (tok0 + u * step) * kTcRows);
-          v[u][0] += p.x;
-          v[u][1] += p.y;
-          v[u][2] += p.z;
-          v[u][3] += p.w;
+        const int tok = tok0 + u * step;
+        if (tok < a.batch) {
+          float v[4] = {};
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            v[0] += p[u][r].x;
+            v[1] += p[u][r].y;
+            v[2] += p[u][r].z;
+            v[3] += p[u][r].w;
+          }
+          T* out = static_cast<T*>(a.out) + tok * a.out_stride + n;
+          T o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = W4Type<T>::from_f32(v[i] + bias[i]);
+          if (whole) {
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (n + i < a.n_out) out[i] = o[i];
+          }
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int tok = tok0 + u * step;
-      if (tok < a.batch) {
-        T* out = static_cast<T*>(a.out) + tok * a.out_stride + n;
-        T o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = W4Type<T>::from_f32(v[u][i] + bias[i]);
-        if (whole) {
-          *reinterpret_cast<uint2*>(out) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (n + i < a.n_out) out[i] = o[i];
-        }
-      }
-    }
+  };
+  switch (S) {
+    case 1: add(std::integral_constant<int, 1>()); break;
+    case 2: add(std::integral_constant<int, 2>()); break;
+    case 4: add(std::integral_constant<int, 4>()); break;
+    default: add(std::integral_constant<int, 8>()); break;
   }
   cluster.sync();  // no CTA leaves while another reads its sums
 }
@@ -337,9 +350,13 @@ int launch_linear_tc(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t s
   const int rc = host_raise_smem(kern, kTcSmem, dev, raised);
   if (rc != MOE_OK) return rc;
   const int row_blocks = (a.n_panels * 16 + kTcRows - 1) / kTcRows;
-  // as many CTAs for K as fit one to an SM, with a step each at least
+  // as many CTAs for K as fit one to an SM, with a step each at least; 8 for no
+  // more than 8 clusters: not every GPC has room for two clusters of 8 whole SMs,
+  // and 16 of them took two waves (K 7,168, 4,096 outputs, 32 tokens: 21 us in
+  // clusters of 8, 14.7 in clusters of 4; 1,024 outputs, 17 tokens: 10.3 and 13.4)
+  const int most = row_blocks <= 8 ? 8 : 4;
   int s = 1;
-  while (s < 8 && 2 * s * row_blocks <= num_sms && a.geom.tiles >= 4 * s) s *= 2;
+  while (s < most && 2 * s * row_blocks <= num_sms && a.geom.tiles >= 4 * s) s *= 2;
   const cudaError_t e =
       host_launch(kern, dim3((unsigned)(row_blocks * s)), kW4TcThreads, kTcSmem, st, s, true, a);
   return e == cudaSuccess ? MOE_OK : host_fail_cuda(e);
