@@ -73,11 +73,12 @@ def test_block_handle_shapes(lib):
         return lib.moe_decode_workspace_bytes(ctypes.byref(mdb.Shapes(**d)))
 
     plain = ws(flags=0)
-    # a row for every (token, choice) and the shared expert; above 16 tokens lists of 1,088 and 1,024 units besides
+    # a row for every (token, choice) and the shared expert; above 8 tokens lists of 1,088 and 1,024 units besides
     lists = (16 + 3 * (1088 + 1024) * 4 + 255) // 256 * 256
     assert ws() == plain + 64 * 9 * 7168 * 4 + lists
     assert ws(n_shared=0, shared_inter=0) == ws(n_shared=0, shared_inter=0, flags=0) + 64 * 8 * 7168 * 4 + lists
-    assert ws(max_batch=16) == ws(max_batch=16, flags=0) + 16 * 9 * 7168 * 4
+    assert ws(max_batch=16) == ws(max_batch=16, flags=0) + 16 * 9 * 7168 * 4 + lists
+    assert ws(max_batch=8) == ws(max_batch=8, flags=0) + 8 * 9 * 7168 * 4
     assert ws(flags=mdb.MOE_FLAG_W4_WEIGHTS | mdb.MOE_FLAG_PARTIAL_SUM) == ws()
     for kw in (dict(hidden=7168 + 32), dict(inter=2048 + 32), dict(shared_inter=2048 + 32)):
         assert ws(**kw) == 0, kw
