@@ -221,23 +221,27 @@ struct BalanceRows {
         continue;
       }
       m = warp_max(m);
-      const bool some = m != -INFINITY;  // (NaN counts as some)
+      // (fmaxf drops NaN, so a row of NaN and -inf alone has none either: its
+      // sums are NaN, and so are the loss and the row's gradient)
+      const bool some = m != -INFINITY;
       float sum = 0.f, dot = 0.f;
       auto take = [&](float& v, float arg, float cc) {
         v = exp2_fast(arg);
         sum += v;
         dot = fmaf(v, cc, dot);
       };
-      if (fabsf(m) < 0x1p+100f) {
-        // one rounding more of m log2(e), the same for the whole row: it drops out
+      if (fabsf(m) < 0x1p+20f) {
+        // one rounding more of m log2(e), the same for the whole row: below 2^-4,
+        // so no exponential leaves its range, and it drops out
         const float ml = m * kLog2e;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) take(ex[i][j], fmaf(ex[i][j], kLog2e, -ml), c[i][j]);
       } else {
-        // the difference before the product with log2(e): the type's lowest
-        // value times log2(e) would be -inf, and a row of it a NaN
+        // the difference before the product with log2(e): at 2^31 the rounding
+        // above would be 128 (a row of 2^128 or of 0: NaN), and the type's lowest
+        // value times log2(e) -inf
         const float top = some ? m : 0.f;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
