@@ -66,7 +66,9 @@ extern "C" {
 #define MOE_ERR_CUDA (-5)              /* a CUDA runtime call failed; see moe_decode_last_cuda_error */
 #define MOE_ERR_OUT_OF_MEMORY (-6)     /* workspace allocation failed in init */
 #define MOE_ERR_DEVICE_TIMEOUT (-7)    /* a bounded device-side wait gave up (status word) */
-#define MOE_ERR_DEVICE_PLAN (-8)       /* device-side consistency check failed (status word) */
+#define MOE_ERR_DEVICE_PLAN (-8)       /* device-side consistency check failed (status word): NaN logits left a
+                                          token fewer than top_k experts to choose (its ids are distinct all the
+                                          same, its other ids arbitrary) */
 
 /* ---------------------------------------------------------------- shapes */
 /*

@@ -155,6 +155,25 @@ __device__ __forceinline__ void warp_top8(const float* lg, const float* bias, in
   }
 }
 
+// Logits that are NaN rank nowhere, so fewer than k of a token may have been
+// found, and where k > 8 the lanes may disagree about a round's winner.  The
+// plan stays well formed all the same: a token's ids are always distinct (the
+// expert kernels have room for one assignment of a token to an expert).  Of the
+// lanes < k, those in `left` have no id of their own: each takes the first free
+// one from its own number on, and the status word tells.  All lanes call it.
+static __device__ __noinline__ int router_free_ids(unsigned left, int my_id, int lane, int k, int E, int* status) {
+  for (; left != 0u; left &= left - 1u) {
+    const int f = __ffs(left) - 1;
+    int c = f;
+    while (__any_sync(0xffffffffu, lane < k && ((left >> lane) & 1u) == 0u && my_id == c)) c = c + 1 == E ? 0 : c + 1;
+    if (lane == f) {
+      atomicCAS(status, kStatusOk, kStatusPlan);
+      my_id = c;
+    }
+  }
+  return my_id;
+}
+
 // Exclusive scan of one int per thread over the block (NT threads).
 template <int NT>
 __device__ __forceinline__ int block_exclusive_scan(int v, int* warp_tot, int& total) {
@@ -323,10 +342,13 @@ __global__ void __launch_bounds__(router_threads(NV), 1) router_topk_kernel(cons
   // lanes j < k of a warp hold token t's selection in order: the ids, their
   // renormalised weights p_j / sum_S p = exp(l_j - l_max) / sum_S exp(l_i - l_max)
   auto finish_token = [&](int t, int my_id, float my_v) {
-    if (lane < k && (my_id < 0 || my_id >= E)) {  // cannot happen for k <= E; keep the plan valid
-      atomicCAS(a.status, kStatusOk, kStatusPlan);
-      my_id = lane;
+    bool bad = lane < k && (my_id < 0 || my_id >= E);
+    if (k > 8) {  // a lower lane has the same
+      const unsigned same = __match_any_sync(0xffffffffu, lane < k ? my_id : ~lane);
+      bad = bad || (lane < k && (same & ((1u << lane) - 1u)) != 0u);
     }
+    const unsigned left = __ballot_sync(0xffffffffu, bad);
+    if (left != 0u) my_id = router_free_ids(left, my_id, lane, k, E, a.status);
     const float lmax = __shfl_sync(0xffffffffu, my_v, 0);
     const float ex = (lane < k) ? expf(my_v - lmax) : 0.f;
     float sum = ex;
@@ -378,7 +400,7 @@ __global__ void __launch_bounds__(router_threads(NV), 1) router_topk_kernel(cons
     float* cand_v = s_w + kMaxAssign / 2;  // [32]
     int* cand_i = s_ids + kMaxAssign / 2;
     const float v = tid < E ? s_lg[tid] + s_bias[tid] : -INFINITY;
-    float m = v;
+    float m = fmaxf(v, -INFINITY);  // (a NaN would not sort)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     if (lane == 0) w_max[warp] = m;
@@ -498,15 +520,11 @@ __global__ void __launch_bounds__(router_threads(NV), 1) router_topk_kernel(cons
       float bv = lbv;
       int bi = lbi;
       warp_argmax(bv, bi);
-      if (bi < 0 || bi >= E) {  // cannot happen for k <= E; keep the plan valid
-        atomicCAS(a.status, kStatusOk, kStatusPlan);
-        bi = j;
-      }
       if (lane == j) {
         my_id = bi;
         my_v = bv;
       }
-      if ((bi & 31) == lane) {
+      if (bi < E && (bi & 31) == lane) {
         taken |= 1u << (bi >> 5);
         local_best(lbv, lbi);
       }
