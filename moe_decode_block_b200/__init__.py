@@ -183,6 +183,17 @@ def _current_stream(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+_W4_TYPES = []
+
+
+def _w4_types() -> list:
+    """bfloat16, float32 and int32: the types of forward_w4's tensors."""
+    if not _W4_TYPES:
+        import torch
+        _W4_TYPES.extend((torch.bfloat16, torch.float32, torch.int32))
+    return _W4_TYPES
+
+
 def _packed_w4_bytes(n: int, k: int, group: int, zeros: bool) -> int:
     """Bytes of a packed 4-bit matrix of sizes that the library accepts."""
     return (n + 15) // 16 * (k // 64 * 512 + k // group * (64 if zeros else 32))
@@ -321,24 +332,44 @@ class MoEDecode:
         """Enqueue one forward with 4-bit expert weights (handle made with
         w4=True): w13 / w2 [E, panels, panel bytes] uint8 (or lists of E) in
         packed form (w4.pack), shared_w13 / shared_w2 likewise without the E
-        axis; group and zeros as the matrices were packed."""
+        axis; group and zeros as the matrices were packed.  x bf16 [B, H],
+        router_w bf16 [H, E], out bf16 [B, H] (float32 with partial=True; not
+        x), topk_ids int32 [B, k] and topk_w float32 [B, k]: contiguous, on
+        the handle's GPU, of `batch` rows or more."""
         if batch is None:
             batch = x.shape[0]
+        dev, sh = self._device, self.shapes
+        H, I, Is, E, k = sh.hidden, sh.inter, sh.shared_inter, sh.n_experts, sh.top_k
+        bf16, f32, i32 = _w4_types()
+        out_type = f32 if sh.flags & MOE_FLAG_PARTIAL_SUM else bf16
+        if (x.dtype is not bf16 or router_w.dtype is not bf16 or out.dtype is not out_type or topk_ids.dtype is not i32
+                or topk_w.dtype is not f32 or x.numel() < batch * H or router_w.numel() < H * E or out.numel() < batch * H
+                or topk_ids.numel() < batch * k or topk_w.numel() < batch * k or not x.is_contiguous()
+                or not router_w.is_contiguous() or not out.is_contiguous() or not topk_ids.is_contiguous()
+                or not topk_w.is_contiguous() or x.get_device() != dev or router_w.get_device() != dev
+                or out.get_device() != dev or topk_ids.get_device() != dev or topk_w.get_device() != dev):
+            for name, t, dtype, least in (("x", x, bf16, batch * H), ("router_w", router_w, bf16, H * E),
+                                          ("out", out, out_type, batch * H), ("topk_ids", topk_ids, i32, batch * k),
+                                          ("topk_w", topk_w, f32, batch * k)):
+                if t.dtype is not dtype or t.numel() < least or not t.is_contiguous() or t.get_device() != dev:
+                    raise ValueError(f"{name}: expected at least {least} contiguous elements of {dtype} on GPU {dev}, "
+                                     f"got {tuple(t.shape)} of {t.dtype} on {t.device}, strides {tuple(t.stride())}")
         if group in (32, 64, 128):  # (another is the library's to refuse)
-            sh = self.shapes
-            H, I, Is = sh.hidden, sh.inter, sh.shared_inter
-            for name, w, n, k in (("w13", w13, 2 * I, H), ("w2", w2, H, I), ("shared_w13", shared_w13, 2 * Is, H),
-                                  ("shared_w2", shared_w2, H, Is)):
-                need = _packed_w4_bytes(n, k, group, zeros)
+            for name, w, n, kk in (("w13", w13, 2 * I, H), ("w2", w2, H, I), ("shared_w13", shared_w13, 2 * Is, H),
+                                   ("shared_w2", shared_w2, H, Is)):
+                need = _packed_w4_bytes(n, kk, group, zeros)
                 if hasattr(w, "data_ptr"):
                     stacked = not name.startswith("shared")
                     got = w.numel() * w.element_size()
-                    if got != need * (sh.n_experts if stacked else 1) or not w.is_contiguous():
+                    if got != need * (E if stacked else 1) or not w.is_contiguous():
                         raise ValueError(f"{name}: expected {need} contiguous bytes per matrix, got {got} in all")
+                    if w.get_device() != dev:
+                        raise ValueError(f"{name}: on {w.device}, the handle is on GPU {dev}")
                 elif isinstance(w, (list, tuple)):
                     for t in w:
-                        if hasattr(t, "data_ptr") and (t.numel() * t.element_size() != need or not t.is_contiguous()):
-                            raise ValueError(f"{name}: expected {need} contiguous bytes per matrix")
+                        if hasattr(t, "data_ptr") and (t.numel() * t.element_size() != need or not t.is_contiguous()
+                                                       or t.get_device() != dev):
+                            raise ValueError(f"{name}: expected {need} contiguous bytes per matrix on GPU {dev}")
         sm = _current_stream(self._device) if stream is None else _stream_handle(stream)
         rc = self._lib.moe_decode_forward_w4(self._h, x.data_ptr(), router_w.data_ptr(), self._table(w13),
                                              self._table(w2), _ptr(shared_w13), _ptr(shared_w2), out.data_ptr(),
