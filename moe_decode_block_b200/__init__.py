@@ -265,7 +265,8 @@ class MoEDecode:
         h = ctypes.c_void_p()
         _check(self._lib.moe_decode_init(ctypes.byref(self.shapes), ctypes.byref(h)), "moe_decode_init")
         self._h = h
-        self._device = _current_device()
+        import torch
+        self._device = torch.cuda.current_device()
         self._aux = None
         self._tables = {}
 
