@@ -366,10 +366,11 @@ int moe_w4_pack(const void* codes, const void* scales, const void* zeros, void* 
  *   packed : device, the matrix in packed form, 16-byte aligned
  *   bias   : device [out] or NULL
  *   out    : device [batch, out], rows out_stride >= out elements apart;
- *            elements between rows are not written; must not overlap x
+ *            elements between rows are not written; a row that shares bytes
+ *            with a row of x is refused (columns of one buffer are not)
  *   dtype  : type of x, bias, out and of the packed scales (MOE_DTYPE_BF16 or
  *            MOE_DTYPE_FP16); batch 0 reads and writes nothing
- * Errors: as moe_w4_pack.
+ * Errors: as moe_w4_pack; MOE_ERR_INVALID_ARG also for out on x.
  */
 int moe_w4_linear(const void* x, const void* packed, const void* bias, void* out, int32_t batch, int32_t in_features,
                   int32_t out_features, int32_t group, int32_t has_zeros, int64_t x_stride, int64_t out_stride,

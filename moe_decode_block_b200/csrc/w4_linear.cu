@@ -322,6 +322,24 @@ bool w4_shape_ok(int n_out, int k, int group) {
 
 bool dtype_ok(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP16; }
 
+// Whether a row of out shares bytes with a row of x (rows of 16-bit elements
+// whose bounding ranges may interleave, as columns of one buffer do).
+bool rows_meet(const void* x, long long x_stride, int k, const void* out, long long out_stride, int n, int batch) {
+  const auto span = [&](const void* p, long long stride, int row) {
+    return reinterpret_cast<uintptr_t>(p) + (uintptr_t)(row * stride) * 2;
+  };
+  const int last = batch - 1;
+  if (span(x, x_stride, last) + 2 * (uintptr_t)k <= reinterpret_cast<uintptr_t>(out) ||
+      span(out, out_stride, last) + 2 * (uintptr_t)n <= reinterpret_cast<uintptr_t>(x))
+    return false;
+  for (int i = 0; i < batch; ++i)
+    for (int j = 0; j < batch; ++j) {
+      const uintptr_t a = span(x, x_stride, i), b = span(out, out_stride, j);
+      if (a < b + 2 * (uintptr_t)n && b < a + 2 * (uintptr_t)k) return true;
+    }
+  return false;
+}
+
 // Cluster size (CTAs that split K): as many as fill two CTAs on every SM, as
 // long as every warp keeps a step of its own.
 int cluster_for(int row_blocks, int steps, int slots) {
@@ -423,6 +441,7 @@ int moe_w4_linear(const void* x, const void* packed, const void* bias, void* out
   if (!host_aligned(x, 16) || !host_aligned(packed, 16) || !host_aligned(out, 2) || !host_aligned(bias, 2))
     return MOE_ERR_INVALID_ARG;
   if (batch > 1 && (x_stride % 8 || x_stride < 0 || out_stride < out_features)) return MOE_ERR_INVALID_ARG;
+  if (rows_meet(x, x_stride, in_features, out, out_stride, out_features, batch)) return MOE_ERR_INVALID_ARG;
   int dev, sms;
   const int rc = host_current_device(&dev, &sms);
   if (rc != MOE_OK) return rc;

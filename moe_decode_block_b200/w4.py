@@ -108,7 +108,8 @@ def _refuse_linear(x, packed, out, group, zeros, bias):
 def linear(x, packed, out, group: int, zeros: bool = False, bias=None, stream=None):
     """out[b, n] = bias[n] + sum_k x[b, k] W[n, k]: x [B, K], out [B, N] (rows
     may be strided, elements not), packed the [N, K] matrix from pack(), bias
-    [N] or None; all of one 16-bit type.  `stream` belongs to x's device."""
+    [N] or None; all of one 16-bit type; no row of out on a row of x.  `stream`
+    belongs to x's device."""
     B, K = x.shape
     Bo, N = out.shape
     sx, so = x.stride(), out.stride()
