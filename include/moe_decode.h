@@ -356,8 +356,9 @@ int moe_w4_pack(const void* codes, const void* scales, const void* zeros, void* 
  * layer on a packed 4-bit matrix for 1 .. MOE_W4_MAX_BATCH tokens.  Products
  * and sums in fp32, one rounding to the type of x in the end.  Up to 16 tokens
  * no weight is rounded; above, each weight s (q - z) is rounded once to the type
- * of x (s below 2^27 in bf16, below 128 in fp16).  An infinite activation may
- * give NaN; |x| in bf16 is held from 2^-57 to 2^63 up to 16 tokens.
+ * of x, which has to hold it; in bf16 scales are then below 2^27 (2^122 with zero
+ * points).  An infinite activation may give NaN; |x| in bf16 is held from 2^-57 to
+ * 2^63 up to 16 tokens.
  * Deterministic.  Asynchronous on `stream` of the current device, one kernel,
  * no workspace, nothing kept between calls: calls may overlap on any streams
  * and be captured in CUDA graphs.
@@ -395,11 +396,13 @@ int moe_w4_linear_status(void* stream);
  *   w2  : HOST array of n_experts device pointers -> packed [hidden, inter]
  *   shared_w13, shared_w2 : device, packed (NULL iff n_shared == 0)
  *   group, has_zeros : of every matrix; scales (and zero points) in bf16
- * Products and sums in fp32.  Up to 8 tokens no weight is rounded; above, the
- * shared expert and the experts that more than 8 tokens chose take each
- * weight s (q - z) rounded once to bf16 (s below 2^27).  The experts' products
- * are added in a fixed order: the outputs are the same bits on every call with
- * the same routing weights.  Stage counters of
+ * Products and sums in fp32; the SwiGLU activations go to the down projection in
+ * bf16, as in the bf16 block (half a step, 2^-8 of each: the same order as the
+ * rounding of `out`, and half the bytes between the two kernels).  Up to 8 tokens
+ * no weight is rounded; above, the shared expert and the experts that more than 8
+ * tokens chose take each weight s (q - z) rounded once to bf16 (scales as for
+ * moe_w4_linear).  The experts' products are added in a fixed order: the outputs
+ * are the same bits on every call with the same routing weights.  Stage counters of
  * moe_decode_stats are not kept for this path.  Errors: as
  * moe_decode_forward; MOE_ERR_INVALID_ARG also for a handle made without
  * MOE_FLAG_W4_WEIGHTS, MOE_ERR_UNSUPPORTED_SHAPE for a group that does not

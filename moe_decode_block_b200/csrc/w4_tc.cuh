@@ -13,19 +13,24 @@
 // instance spilled, the change comes above 8 (w4_experts.cuh).
 //
 // Mathematics.  Here a weight s (q - z) is rounded once to the activations' type
-// (half a step: 2^-9 relative in bf16, 2^-12 in fp16; powers of two times s are
-// exact) and the products are summed in fp32 over all of K in tensor memory.  The
+// (half a step: up to 2^-8 of it in bf16, 2^-11 in fp16; it has to fit the type)
+// and the products are summed in fp32 over all of K in tensor memory.  The
 // exact form of w4_core.cuh -- a group's sum read back and scaled in fp32 -- was
 // built too: reading 64 sums a row back every 128 inputs, beside the MMAs' own
 // traffic to tensor memory, took 1,700 clocks a step where the MMAs take 860, 52
 // us for a layer of 16,384 x 7,168 at 64 tokens where the rounded form then took
 // 38.  The rounding adds 6e-4 to the 1.7e-3 that rounding the result to bf16 costs.
 //
-// A code becomes an operand by a mask (a subnormal, as in w4_core.cuh) and, in
-// bf16 without zero points, one fused multiply-add, q (s 2^100) - 8 s 2^-33, whose
-// one rounding is the weight's (times 2^-33, taken off in the end; s below 2^27).
-// Zero points and fp16 take two instructions: (q - z) times a power of two, exact,
-// then the product with the scale times the inverse power (fp16: s below 128).
+// A code becomes an operand by a mask and, in bf16 (where it is a subnormal, as in
+// w4_core.cuh) without zero points, one fused multiply-add, q (s 2^100) - 8 s 2^-33,
+// whose one rounding is the weight's (times 2^-33, taken off in the end; s below
+// 2^27).  Zero points and fp16 take two instructions: q - z, exact, then the product
+// with the scale.  In bf16 that is (q - z) times a power of two, which the scale
+// takes off (s below 2^122); in fp16 the code stands in the lowest bits of 1024 and
+// the scale is as it came, so any that the weights allow will do.  (From subnormal
+// codes fp16 needed s 2^9, which ended at 128.  To hold larger scales in bf16 too,
+// by the two instructions or by a vote of the warp on a step's scales, cost the
+// layer above 1.2 to 2 us of 27, for scales that no model has.)
 //
 // Layout of the work.  A CTA has 256 weight rows (two accumulators of 128) and up
 // to 64 tokens, and takes K in steps of 128 inputs.  Its 16 warps:
@@ -202,8 +207,8 @@ constexpr int kTcWaitLimit = 1 << 15;
 
 __device__ __forceinline__ int tc_columns(int n_tok) { return (n_tok + 15) / 16 * 16; }
 
-// Codes as subnormals to weights.  `low` operands are outputs g's, the others
-// outputs (g + 8)'s, whose codes stand four bits higher.
+// Codes to weights: a word's four operand registers, two of outputs g, then two of
+// outputs g + 8, whose codes stand four bits higher.
 template <typename T, bool ZP>
 struct W4Dequant;
 template <bool ZP>
@@ -233,10 +238,16 @@ struct W4Dequant<__nv_bfloat16, ZP> {
       add[1] = high(c);
     }
   }
-  __device__ __forceinline__ uint32_t operator()(uint32_t code, int hi) const {
-    V t = __hfma2(word(code), mul[hi], add[hi]);
-    if constexpr (ZP) t = __hmul2(t, sc[hi]);
-    return *reinterpret_cast<const uint32_t*>(&t);
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t* r) const {
+    uint32_t o[4];
+    w4_operands(w, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int hi = i >> 1;
+      V t = __hfma2(word(o[2 * (i & 1) + hi]), mul[hi], add[hi]);
+      if constexpr (ZP) t = __hmul2(t, sc[hi]);
+      r[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
   }
 };
 template <bool ZP>
@@ -247,17 +258,30 @@ struct W4Dequant<__half, ZP> {
   static __device__ __forceinline__ V pair(float lo, float hi) { return __floats2half2_rn(lo, hi); }
   static __device__ __forceinline__ V word(uint32_t w) { return *reinterpret_cast<const V*>(&w); }
   __device__ __forceinline__ void set(uint32_t s, uint32_t z) {
-    // 2^-24 q 2^15 - z 2^-9 (outputs g + 8: 2^-5), times s 2^9 (2^5)
-    const V k = __hmul2(word(s), pair(0x1p+9f, 0x1p+5f));
-    const V c = __hmul2(ZP ? word(z) : pair(8.f, 8.f), pair(-0x1p-9f, -0x1p-5f));
+    // (1024 + q) - (1024 + z); outputs g + 8: (1024 + 16 q) / 16 - (64 + z)
+    const V c = __hneg2(__hadd2(ZP ? word(z) : pair(8.f, 8.f), pair(1024.f, 64.f)));
     add[0] = __low2half2(c);
     add[1] = __high2half2(c);
-    sc[0] = __low2half2(k);
-    sc[1] = __high2half2(k);
+    sc[0] = __low2half2(word(s));
+    sc[1] = __high2half2(word(s));
   }
-  __device__ __forceinline__ uint32_t operator()(uint32_t code, int hi) const {
-    const V t = __hmul2(__hfma2(word(code), pair(0x1p+15f, 0x1p+15f), add[hi]), sc[hi]);
-    return *reinterpret_cast<const uint32_t*>(&t);
+  // `base`: two of 1024, in a register of its own so that mask and bits are one
+  // instruction (as two they cost the layer 3.5 us of 29)
+  static __device__ __forceinline__ V code(uint32_t w, uint32_t mask, uint32_t base) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xf8;" : "=r"(r) : "r"(base), "r"(w), "r"(mask));  // base | (w & mask)
+    return word(r);
+  }
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t* r) const {
+    uint32_t base = 0x64006400u;
+    asm("" : "+r"(base));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int hi = i >> 1;
+      const V v = code(i & 1 ? w >> 8 : w, hi ? 0x00f000f0u : 0x000f000fu, base);
+      const V t = __hmul2(__hfma2(v, hi ? pair(0x1p-4f, 0x1p-4f) : pair(1.f, 1.f), add[hi]), sc[hi]);
+      r[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
   }
 };
 
@@ -511,15 +535,7 @@ __device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Item
           const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
           uint32_t r[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const W4Dequant<T, ZP>& q = dq[p][(ti * kW4Tile + 16 * i) / GROUP];
-            uint32_t o[4];
-            w4_operands(w[i], o);
-            r[4 * i] = q(o[0], 0);
-            r[4 * i + 1] = q(o[2], 0);
-            r[4 * i + 2] = q(o[1], 1);
-            r[4 * i + 3] = q(o[3], 1);
-          }
+          for (int i = 0; i < 4; ++i) dq[p][(ti * kW4Tile + 16 * i) / GROUP](w[i], r + 4 * i);
           tc5_store_operands(a + ((uint32_t)(16 * p) << 16) + 32u * ti, r);
         }
         slot = (slot + 2 * kW4TileBytes) % kTcRingBytes;

@@ -55,7 +55,8 @@ def pack(codes, scales, zeros=None, out=None, stream=None):
     2 j in the low half of byte j), scales [..., N, K / group] bfloat16 or
     float16, zeros [..., N, K / group] uint8 or None -> uint8
     [..., ceil(N / 16), panel bytes].  Leading axes (experts) are packed one
-    matrix at a time."""
+    matrix at a time.  Scales are kept as they are (linear() says which range
+    its products hold); zero points 0..15, the low four bits count."""
     import torch
     lib = load_library()
     if codes.dtype is not torch.uint8 or codes.dim() < 2 or not codes.is_cuda:
@@ -109,7 +110,12 @@ def linear(x, packed, out, group: int, zeros: bool = False, bias=None, stream=No
     """out[b, n] = bias[n] + sum_k x[b, k] W[n, k]: x [B, K], out [B, N] (rows
     may be strided, elements not), packed the [N, K] matrix from pack(), bias
     [N] or None; all of one 16-bit type; no row of out on a row of x.  `stream`
-    belongs to x's device."""
+    belongs to x's device.
+
+    Sums in fp32.  Up to 16 tokens no weight is rounded; |x| in bfloat16 is
+    held from 2^-57 to 2^63 and an infinite activation gives NaN.  Above 16
+    each weight s (q - z) is rounded once to x's type, which has to hold it;
+    scales in bfloat16 are then below 2^27 (2^122 with zero points)."""
     B, K = x.shape
     Bo, N = out.shape
     sx, so = x.stride(), out.stride()
