@@ -388,6 +388,23 @@ int moe_w4_linear(const void* x, const void* packed, const void* bias, void* out
 int moe_w4_linear_status(void* stream);
 
 /*
+ * Bound of the device-side waits of later moe_w4_linear calls of this process,
+ * in probes of up to 20 us; 0, or more than the default, sets the default
+ * (32,768: 2/3 s).  The block's are bounded by moe_decode_set_wait_limit.
+ */
+int moe_w4_linear_set_wait_limit(uint32_t probes);
+
+/*
+ * Testing only: in each of the next `launches` tcgen05 kernels of 4-bit products
+ * that this process launches (one for a moe_w4_linear of more than 16 tokens, two
+ * for a moe_decode_forward_w4 of more than 8) the first CTA never hands over its
+ * first step of activations, so the waits for it run out: the outputs are wrong
+ * and the status says MOE_ERR_DEVICE_TIMEOUT.  Used with a short wait limit to
+ * test that path without faulting or hanging the GPU; 0 takes it back.
+ */
+int moe_w4_test_hold(int32_t launches);
+
+/*
  * moe_decode_forward with 4-bit expert weights (a handle created with
  * MOE_FLAG_W4_WEIGHTS).  x, router_w, out, topk_ids, topk_w and batch as for
  * moe_decode_forward; four kernels on `stream`, seven above 8 tokens.

@@ -37,7 +37,7 @@ EXPORTED = (
     "moe_decode_set_timing_events", "moe_decode_set_wait_limit", "moe_router_topk_noalloc",
     "moe_router_topk_noalloc_status", "moe_decode_reduce_residual",
     "moe_decode_forward_w4", "moe_w4_packed_bytes", "moe_w4_pack", "moe_w4_linear",
-    "moe_w4_linear_status",
+    "moe_w4_linear_status", "moe_w4_linear_set_wait_limit", "moe_w4_test_hold",
     "moe_balance_workspace_bytes", "moe_balance_loss",
 )
 MOE_TIMING_EVENTS = 6
@@ -136,6 +136,10 @@ def load_library() -> ctypes.CDLL:
     lib.moe_w4_linear.restype = I
     lib.moe_w4_linear_status.argtypes = [P]
     lib.moe_w4_linear_status.restype = I
+    lib.moe_w4_linear_set_wait_limit.argtypes = [ctypes.c_uint32]
+    lib.moe_w4_linear_set_wait_limit.restype = I
+    lib.moe_w4_test_hold.argtypes = [i32]
+    lib.moe_w4_test_hold.restype = I
     lib.moe_balance_workspace_bytes.argtypes = [i32]
     lib.moe_balance_workspace_bytes.restype = ctypes.c_uint64
     lib.moe_balance_loss.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i64, i64, ctypes.c_float, i32, P, P]

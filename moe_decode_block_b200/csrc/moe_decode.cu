@@ -792,6 +792,7 @@ int enqueue_forward_w4(moe_decode_ctx* h, const void* x, const void* router_w, c
       moe::W4ExpertArgs t = args(is_down, moe::kTcRows);
       t.n_su = s.n_shared;
       t.units = heavy;
+      t.hold = moe::host_w4_hold();
       const W4Kernel tk = is_down ? pick_w4_tc<true>(group, zeros) : pick_w4_tc<false>(group, zeros);
       const int many = assigned / (moe::kW4LightTokens + 1);
       err = launch(tk, grid_for(t, many < most ? many : most, 1), moe::kW4TcThreads, (size_t)moe::kTcSmem, sm, true, t, tab);

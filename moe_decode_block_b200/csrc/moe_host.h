@@ -33,6 +33,10 @@ int host_raise_smem(K kern, int bytes, int dev, std::atomic<uint64_t>& done) {
   return MOE_OK;
 }
 
+// Whether the next launch of a tcgen05 4-bit kernel holds its first step back
+// (moe_w4_test_hold); counts it.
+int host_w4_hold();
+
 // Launch with an optional cluster size and programmatic dependent launch.
 template <typename... KArgs, typename... Args>
 cudaError_t host_launch(void (*kern)(KArgs...), dim3 grid, int block, size_t smem, cudaStream_t st, int cluster,

@@ -69,6 +69,7 @@ struct W4ExpertArgs {
   int beside;
   int* status;    // w4_expert_tc_kernel: status word and limit of its waits
   int wait_limit;
+  int hold;       // testing: see w4_tc_stage
 };
 
 // An item's unit: loaded one item before the lane's tokens are, which are
@@ -446,7 +447,8 @@ __global__ void __launch_bounds__(kW4TcThreads, 1)
   } else if (warp == kTcMmaWarp) {
     w4_tc_mma<T>(w4_smem, bars, items, a.status);
   } else {
-    w4_tc_stage<T, kTcStagers>(w4_smem, bars, items, warp - kTcMmaWarp - 1, a.status);
+    w4_tc_stage<T, kTcStagers>(w4_smem, bars, items, warp - kTcMmaWarp - 1, a.status,
+                               a.hold != 0 && blockIdx.x == 0);
   }
   w4_tc_end(bars);
 }

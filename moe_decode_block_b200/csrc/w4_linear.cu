@@ -25,6 +25,7 @@ struct W4LinearArgs {
   int batch, n_out, n_panels;
   W4Geom geom;
   long long x_stride, out_stride;  // elements between tokens
+  int wait_limit, hold;            // of the tensor-memory kernel (hold: see w4_tc_stage)
 };
 
 // One CTA: 64 outputs x NT * 8 tokens x its share of K; the 8 warps split
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
 
   // (tensor memory is held before the next kernel may come: one that takes tensor
   // memory first and then waits for this grid would never end)
-  w4_tc_begin(bars, kTcWaitLimit);
+  w4_tc_begin(bars, a.wait_limit);
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   int* status = &g_w4_linear_status;
@@ -194,7 +195,8 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
   else if (warp == kTcMmaWarp)
     w4_tc_mma<T>(w4_smem, bars, items, status);
   else if (warp - kTcUnpackers - (warp > kTcMmaWarp) < kTcSlots)
-    w4_tc_stage<T, kTcSlots>(w4_smem, bars, items, warp - kTcUnpackers - (warp > kTcMmaWarp), status);
+    w4_tc_stage<T, kTcSlots>(w4_smem, bars, items, warp - kTcUnpackers - (warp > kTcMmaWarp), status,
+                             a.hold != 0 && blockIdx.x == 0);
 
   // then every warp takes 16 tokens of its quarter of both accumulators' rows
   static_assert(kW4TcThreads == 32 * 4 * (kTcTokens / 16), "a warp's quarter and tokens");
@@ -314,6 +316,18 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* codes, cons
 }
 
 namespace {
+std::atomic<int> g_w4_wait_limit{kTcWaitLimit};  // of moe_w4_linear
+std::atomic<int> g_w4_hold{0};                   // launches left that hold a step back
+}  // namespace
+
+int host_w4_hold() {
+  int n = g_w4_hold.load(std::memory_order_relaxed);
+  while (n > 0 && !g_w4_hold.compare_exchange_weak(n, n - 1, std::memory_order_relaxed)) {
+  }
+  return n > 0;
+}
+
+namespace {
 
 bool w4_shape_ok(int n_out, int k, int group) {
   if (n_out < 1 || n_out > MOE_W4_MAX_OUT || k < kW4Tile || k > MOE_W4_MAX_IN || k % kW4Tile) return false;
@@ -362,7 +376,9 @@ int launch_linear(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) 
 }
 
 template <typename T, int GROUP, bool ZP>
-int launch_linear_tc(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) {
+int launch_linear_tc(W4LinearArgs a, int dev, int num_sms, cudaStream_t st) {
+  a.wait_limit = g_w4_wait_limit.load(std::memory_order_relaxed);
+  a.hold = host_w4_hold();
   static std::atomic<uint64_t> raised{0};
   const auto kern = w4_linear_tc_kernel<T, GROUP, ZP>;
   const int rc = host_raise_smem(kern, kTcSmem, dev, raised);
@@ -461,6 +477,19 @@ int moe_w4_linear(const void* x, const void* packed, const void* bias, void* out
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return dtype == MOE_DTYPE_BF16 ? pick_linear<__nv_bfloat16>(a, group, has_zeros != 0, dev, sms, st)
                                  : pick_linear<__half>(a, group, has_zeros != 0, dev, sms, st);
+}
+
+int moe_w4_linear_set_wait_limit(uint32_t probes) {
+  using namespace moe;
+  g_w4_wait_limit.store(probes == 0 || probes > (uint32_t)kTcWaitLimit ? kTcWaitLimit : (int)probes,
+                        std::memory_order_relaxed);
+  return MOE_OK;
+}
+
+int moe_w4_test_hold(int32_t launches) {
+  if (launches < 0) return MOE_ERR_INVALID_ARG;
+  moe::g_w4_hold.store(launches, std::memory_order_relaxed);
+  return MOE_OK;
 }
 
 int moe_w4_linear_status(void* stream) {

@@ -202,7 +202,7 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* sta
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return tc_wait_long(smem_addr(bar), parity, status, ctl);
 }
-// Probes of a wait by default: 2/3 s.
+// Probes of a wait by default, and at most: 2/3 s.
 constexpr int kTcWaitLimit = 1 << 15;
 
 __device__ __forceinline__ int tc_columns(int n_tok) { return (n_tok + 15) / 16 * 16; }
@@ -375,8 +375,10 @@ __device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, I
 
 // A stager warp (0 .. STAGERS - 1): the B operands of every STAGERS-th step.  `items.row(item,
 // token)` numbers a token's activation row, `items.rows() + items.offset(row)` is it.
+// `hold` (testing): the first step is never handed over, so the waits for it run out.
 template <typename T, int STAGERS, typename Items>
-__device__ __forceinline__ void w4_tc_stage(uint8_t* smem, W4TcBars& bars, Items items, int stager, int* status) {
+__device__ __forceinline__ void w4_tc_stage(uint8_t* smem, W4TcBars& bars, Items items, int stager, int* status,
+                                            bool hold) {
   // (a stager that was one step behind another's next use of its slot would take
   // the phase before for the one it waits for)
   static_assert(STAGERS <= kTcSlots, "a stager's step before step i + 2 kTcSlots has waited for step i's MMAs");
@@ -432,7 +434,7 @@ __device__ __forceinline__ void w4_tc_stage(uint8_t* smem, W4TcBars& bars, Items
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.b_full[at]);
+      if (lane == 0 && !(hold && i == 0)) mbar_arrive(&bars.b_full[at]);
     }
     ci += (uint32_t)steps;
   }

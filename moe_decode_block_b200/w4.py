@@ -147,3 +147,18 @@ def linear_status(stream=None) -> int:
     on the current device (MOE_OK or an MOE_ERR_* code); clears it."""
     dev = _current_device()
     return load_library().moe_w4_linear_status(_current_stream(dev) if stream is None else _stream_handle(stream))
+
+
+def set_wait_limit(probes: int = 0):
+    """Bound of the device-side waits of later linear() calls of this process
+    in probes of up to 20 us (0: the default, 2/3 s)."""
+    _check(load_library().moe_w4_linear_set_wait_limit(int(probes)), "moe_w4_linear_set_wait_limit")
+
+
+def test_hold(launches: int):
+    """Testing only: the first CTA of each of the next `launches` tcgen05
+    kernels never hands over its first step, so its waits run out."""
+    _check(load_library().moe_w4_test_hold(int(launches)), "moe_w4_test_hold")
+
+
+test_hold.__test__ = False  # (not a test itself, where it is imported into one)

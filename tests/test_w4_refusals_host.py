@@ -74,3 +74,11 @@ def test_tensors_elsewhere_are_refused():
     blk._device = 0
     with pytest.raises(ValueError, match="GPU 0"):
         blk.forward_w4(**_args())
+
+
+def test_wait_limit_and_hold_are_set_on_the_host():
+    lib = mdb.load_library()
+    for probes in (1, 512, 1 << 31, 0):
+        assert lib.moe_w4_linear_set_wait_limit(probes) == mdb.MOE_OK
+    assert lib.moe_w4_test_hold(-1) == mdb.MOE_ERR_INVALID_ARG
+    assert lib.moe_w4_test_hold(3) == mdb.MOE_OK and lib.moe_w4_test_hold(0) == mdb.MOE_OK
