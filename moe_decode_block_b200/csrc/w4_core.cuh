@@ -253,11 +253,12 @@ __device__ __forceinline__ void w4_stream_step(W4Stream& st, uint32_t slot, int 
 // FIRST .. FIRST + COUNT of a step's two tiles (in `slot`) times the lane's x (2
 // x 16 bytes per tile and token tile) into acc, in units of 1 / kUnit (outputs g
 // + 8: 16 / kUnit).  A group's sum is scaled once; groups of 128 are cut between
-// the tiles where these are taken one by one.  N <= NT: token tiles that exist.
-template <typename T, typename C, int N, int FIRST, int COUNT>
+// the tiles where these are taken one by one.
+template <typename T, typename C, int FIRST, int COUNT>
 __device__ __forceinline__ void w4_tiles(const uint8_t* slot, const uint4 (&xv)[COUNT][C::NT][2], int lane,
                                          float (&acc)[kW4Panels][C::NT][4]) {
   using W = W4Type<T>;
+  constexpr int N = C::NT;
   constexpr int kGroups = C::kEntries * COUNT / 2 > 0 ? C::kEntries * COUNT / 2 : 1;
   constexpr int kPer = 4 * COUNT / kGroups;  // mma steps of a group
   // B operands, and the groups' z0 sum x: z0 = 8, or 1 where zero points come
@@ -336,10 +337,10 @@ __device__ __forceinline__ void w4_tiles(const uint8_t* slot, const uint4 (&xv)[
 // of its tokens; xp[n] is at the step's first input.  (A token that does not
 // exist has the address of one that does: its column of the products is never
 // stored, and no column sees another.)
-template <typename T, int N, int NT>
+template <typename T, int NT>
 __device__ __forceinline__ void w4_load_x(const T* const (&xp)[NT], int half, uint4 (&xr)[NT][2]) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
+  for (int n = 0; n < NT; ++n) {
     xr[n][0] = *reinterpret_cast<const uint4*>(xp[n] + half * kW4Tile);
     xr[n][1] = *reinterpret_cast<const uint4*>(xp[n] + half * kW4Tile + 32);
   }
@@ -350,39 +351,39 @@ __device__ __forceinline__ void w4_load_x(const T* const (&xp)[NT], int half, ui
 // next step is in its ring slot and refills the slot before; `slot` follows the
 // ring.  One token tile takes both tiles of a step together and has x of the
 // next step on its way meanwhile; more token tiles have registers for one tile
-// ahead only.  N: token tiles that exist.
+// ahead only.
 template <typename T, typename C>
 struct W4X {
   uint4 v[C::NT == 1 ? 4 : 2][1][C::NT][2];  // NT == 1: two steps of two tiles; else two tiles
 };
 template <typename T, typename C>
 __device__ __forceinline__ void w4_first_x(const T* const (&xp)[C::NT], bool second, W4X<T, C>& x) {
-  w4_load_x<T, C::NT>(xp, 0, x.v[0][0]);
+  w4_load_x<T>(xp, 0, x.v[0][0]);
   if constexpr (C::NT == 1)
-    if (second) w4_load_x<T, 1>(xp, 1, x.v[1][0]);
+    if (second) w4_load_x<T>(xp, 1, x.v[1][0]);
 }
-template <typename T, typename C, int N, typename Advance>
-__device__ __forceinline__ void w4_run_tokens(int s0, int s1, int tiles, const uint8_t* ring, uint32_t& slot,
-                                              const T* (&xp)[C::NT], W4X<T, C>& x, int lane,
-                                              float (&acc)[kW4Panels][C::NT][4], Advance& advance) {
+template <typename T, typename C, typename Advance>
+__device__ __forceinline__ void w4_run(int s0, int s1, int tiles, const uint8_t* ring, uint32_t& slot,
+                                       const T* (&xp)[C::NT], W4X<T, C>& x, int lane,
+                                       float (&acc)[kW4Panels][C::NT][4], Advance& advance) {
   auto consumed = [&]() { slot = slot + C::kSlot == C::kDepth * C::kSlot ? 0 : slot + C::kSlot; };
   auto next_x = [&]() {
 #pragma unroll
-    for (int n = 0; n < N; ++n) xp[n] += 2 * kW4Tile;
+    for (int n = 0; n < C::NT; ++n) xp[n] += 2 * kW4Tile;
   };
   if constexpr (C::NT == 1) {
     auto one = [&](int s, uint4 (&c0)[1][1][2], uint4 (&c1)[1][1][2], uint4 (&n0)[1][1][2], uint4 (&n1)[1][1][2]) {
       next_x();
       if (s + 1 < s1) {
-        w4_load_x<T, 1>(xp, 0, n0[0]);
-        if (2 * s + 3 < tiles) w4_load_x<T, 1>(xp, 1, n1[0]);
+        w4_load_x<T>(xp, 0, n0[0]);
+        if (2 * s + 3 < tiles) w4_load_x<T>(xp, 1, n1[0]);
       }
       advance();
       if (2 * s + 1 < tiles) {
         const uint4 c[2][1][2] = {{{c0[0][0][0], c0[0][0][1]}}, {{c1[0][0][0], c1[0][0][1]}}};
-        w4_tiles<T, C, 1, 0, 2>(ring + slot, c, lane, acc);
+        w4_tiles<T, C, 0, 2>(ring + slot, c, lane, acc);
       } else {
-        w4_tiles<T, C, 1, 0, 1>(ring + slot, c0, lane, acc);
+        w4_tiles<T, C, 0, 1>(ring + slot, c0, lane, acc);
       }
       consumed();
     };
@@ -394,48 +395,32 @@ __device__ __forceinline__ void w4_run_tokens(int s0, int s1, int tiles, const u
   } else {
     for (int s = s0; s < s1; ++s) {
       const bool second = 2 * s + 1 < tiles;
-      if (second) w4_load_x<T, N>(xp, 1, x.v[1][0]);
+      if (second) w4_load_x<T>(xp, 1, x.v[1][0]);
       advance();
-      w4_tiles<T, C, N, 0, 1>(ring + slot, x.v[0], lane, acc);
+      w4_tiles<T, C, 0, 1>(ring + slot, x.v[0], lane, acc);
       next_x();
-      if (s + 1 < s1) w4_load_x<T, N>(xp, 0, x.v[0][0]);
-      if (second) w4_tiles<T, C, N, 1, 1>(ring + slot, x.v[1], lane, acc);
+      if (s + 1 < s1) w4_load_x<T>(xp, 0, x.v[0][0]);
+      if (second) w4_tiles<T, C, 1, 1>(ring + slot, x.v[1], lane, acc);
       consumed();
     }
-  }
-}
-// The same for the token tiles at hand (the same number for the whole warp).
-template <typename T, typename C, typename Advance>
-__device__ __forceinline__ void w4_run(int s0, int s1, int tiles, const uint8_t* ring, uint32_t& slot,
-                                       const T* (&xp)[C::NT], W4X<T, C>& x, int n_tok_tiles, int lane,
-                                       float (&acc)[kW4Panels][C::NT][4], Advance& advance) {
-  if constexpr (C::NT == 1) {
-    w4_run_tokens<T, C, 1>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
-  } else {
-    if (n_tok_tiles == 1)
-      w4_run_tokens<T, C, 1>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
-    else
-      w4_run_tokens<T, C, 2>(s0, s1, tiles, ring, slot, xp, x, lane, acc, advance);
   }
 }
 
 // Accumulators, brought back to units of 1, to the warp's sums [token][row].
 template <typename T, typename C>
-__device__ __forceinline__ void w4_store_sums(float* sums, int lane, int n_tok_tiles,
+__device__ __forceinline__ void w4_store_sums(float* sums, int lane,
                                               const float (&acc)[kW4Panels][C::NT][4]) {
   const int g = lane >> 2, t = lane & 3;
   constexpr float u0 = W4Type<T>::kUnit, u1 = W4Type<T>::kUnit / 16.f;
 #pragma unroll
   for (int n = 0; n < C::NT; ++n) {
-    if (n == 0 || n < n_tok_tiles) {
-      float* p = sums + (n * 8 + 2 * t) * kW4SumPitch + g;
+    float* p = sums + (n * 8 + 2 * t) * kW4SumPitch + g;
 #pragma unroll
-      for (int m = 0; m < kW4Panels; ++m) {
-        p[m * 16] = u0 * acc[m][n][0];
-        p[m * 16 + kW4SumPitch] = u0 * acc[m][n][1];
-        p[m * 16 + 8] = u1 * acc[m][n][2];
-        p[m * 16 + 8 + kW4SumPitch] = u1 * acc[m][n][3];
-      }
+    for (int m = 0; m < kW4Panels; ++m) {
+      p[m * 16] = u0 * acc[m][n][0];
+      p[m * 16 + kW4SumPitch] = u0 * acc[m][n][1];
+      p[m * 16 + 8] = u1 * acc[m][n][2];
+      p[m * 16 + 8 + kW4SumPitch] = u1 * acc[m][n][3];
     }
   }
 }

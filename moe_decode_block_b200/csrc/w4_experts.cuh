@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<1, GROUP, ZP, kW4ExpertSplit
       if constexpr (DOWN) s_wt[parity][lane] = ph ? __ldcg(a.assign_w + un.begin + lane) : 1.f;
     }
     float acc[kW4Panels][1][4] = {};
-    w4_run<T, C>(s0, s1, P.geom.tiles, ring, slot, xp, xr, 1, lane, acc, advance);
+    w4_run<T, C>(s0, s1, P.geom.tiles, ring, slot, xp, xr, lane, acc, advance);
     if (next.count > 0) {  // the next item's first activations, under this one's epilogue
       int n0, n1;
       steps_of(next_ph, n0, n1);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<1, GROUP, ZP, kW4ExpertSplit
       if (n0 < n1) w4_first_x<T, C>(xp, 2 * n0 + 1 < a.ph[next_ph].geom.tiles, xr);
     }
     __syncthreads();  // the last item's sums have been read
-    w4_store_sums<T, C>(sums + warp * (C::kSums / 4), lane, 1, acc);
+    w4_store_sums<T, C>(sums + warp * (C::kSums / 4), lane, acc);
     __syncthreads();
 
     // thread: a row (of 128) of every second token; UP: a column (of 64) of every fourth

@@ -52,7 +52,6 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row_blk = blockIdx.x / S;
   const int n_tok = a.batch;
-  const int n_tok_tiles = (n_tok + 7) / 8;
 
   const int q = rank * kW4Warps + warp, Q = S * kW4Warps;
   const int steps = w4_steps(a.geom);
@@ -96,10 +95,10 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
   float acc[kW4Panels][NT][4] = {};
   W4X<T, C> xr;
   if (s0 < s1) w4_first_x<T, C>(xp, 2 * s0 + 1 < a.geom.tiles, xr);
-  w4_run<T, C>(s0, s1, a.geom.tiles, ring, slot, xp, xr, n_tok_tiles, lane, acc, advance);
+  w4_run<T, C>(s0, s1, a.geom.tiles, ring, slot, xp, xr, lane, acc, advance);
   float* base = reinterpret_cast<float*>(w4_smem + C::kRing);
   constexpr int kStride = C::kSums / 4;
-  w4_store_sums<T, C>(base + warp * kStride, lane, n_tok_tiles, acc);
+  w4_store_sums<T, C>(base + warp * kStride, lane, acc);
   cp_async_wait<0>();
   const float* sums[kW4Warps];
 #pragma unroll
@@ -366,7 +365,7 @@ template <typename T, int NT, int GROUP, bool ZP>
 int launch_linear(const W4LinearArgs& a, int dev, int num_sms, cudaStream_t st) {
   using C = W4Cfg<NT, GROUP, ZP, kW4Warps>;
   static std::atomic<uint64_t> raised{0};
-  const auto kern = w4_linear_kernel<T, NT, GROUP, ZP>;
+  const auto kern = w4_linear_kernel<T, NT, GROUP, ZP>;  // (NT token tiles: 8 (NT - 1) < batch <= 8 NT)
   const int rc = host_raise_smem(kern, C::kSmem, dev, raised);
   if (rc != MOE_OK) return rc;
   const int row_blocks = (a.n_panels + kW4Panels - 1) / kW4Panels;
