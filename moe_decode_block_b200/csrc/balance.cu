@@ -28,12 +28,10 @@
 // of more tokens take 10.3 us from 513 to 2,048.
 #include <cooperative_groups.h>
 
-#include <atomic>
-
-#include "moe_host.h"
-#include "moe_device.cuh"
-
 #include <cuda_fp16.h>
+
+#include "moe_device.cuh"
+#include "moe_host.h"
 
 namespace moe {
 
