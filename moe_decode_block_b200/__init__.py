@@ -375,10 +375,13 @@ class MoEDecode:
                         if hasattr(t, "data_ptr") and (t.numel() * t.element_size() != need or not t.is_contiguous()
                                                        or t.get_device() != dev):
                             raise ValueError(f"{name}: expected {need} contiguous bytes per matrix on GPU {dev}")
+        else:
+            group = 0  # (beyond 32 bits it must not come around to one of them)
         sm = _current_stream(self._device) if stream is None else _stream_handle(stream)
         rc = self._lib.moe_decode_forward_w4(self._h, x.data_ptr(), router_w.data_ptr(), self._table(w13),
                                              self._table(w2), _ptr(shared_w13), _ptr(shared_w2), out.data_ptr(),
-                                             topk_ids.data_ptr(), topk_w.data_ptr(), batch, group, 1 if zeros else 0,
+                                             topk_ids.data_ptr(), topk_w.data_ptr(), max(batch, -1), group,
+                                             1 if zeros else 0,
                                              sm)
         _check(rc, "moe_decode_forward_w4")
 

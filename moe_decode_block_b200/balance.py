@@ -11,6 +11,7 @@ from . import (MOE_DTYPE_BF16, MOE_DTYPE_FP16, MOE_DTYPE_FP32, _check, _current_
 from .w4 import _on
 
 ONE_LAUNCH = 512  # tokens up to which no workspace is needed
+MAX_TOKENS = 1 << 24
 _TYPES = {}
 _WORKSPACE = {}
 
@@ -76,8 +77,8 @@ def balance_loss(logits, topk_ids, loss, counts, token_mask=None, router_bias=No
     call = load_library().moe_balance_loss
     args = (logits.data_ptr(), None if router_bias is None else router_bias.data_ptr(), topk_ids.data_ptr(),
             None if token_mask is None else token_mask.data_ptr(), loss.data_ptr(), counts.data_ptr(),
-            None if dlogits is None else dlogits.data_ptr(), None if grad_loss is None else grad_loss.data_ptr(), T, E, k,
-            zs[0], ds[0], coef, code, None if workspace is None else workspace.data_ptr())
+            None if dlogits is None else dlogits.data_ptr(), None if grad_loss is None else grad_loss.data_ptr(),
+            min(T, MAX_TOKENS + 1), E, k, zs[0], ds[0], coef, code, None if workspace is None else workspace.data_ptr())  # (T: 32 bits there)
     if dev == _current_device():
         rc = call(*args, _current_stream(dev) if stream is None else _stream_handle(stream))
     else:

@@ -14,7 +14,8 @@ from contextlib import nullcontext
 from . import (MOE_DTYPE_BF16, MOE_DTYPE_FP16, _check, _current_device, _current_stream, _stream_handle,
                load_library)
 
-MAX_BATCH = 64
+MAX_BATCH = 64       # of linear()
+MAX_SIZE = 1 << 20   # above MOE_W4_MAX_IN and MOE_W4_MAX_OUT
 _CODES = {}
 
 
@@ -44,7 +45,9 @@ def _on(device):
 
 def packed_bytes(out_features: int, in_features: int, group: int, zeros: bool = False) -> int:
     """Bytes of a packed [out_features, in_features] matrix."""
-    n = load_library().moe_w4_packed_bytes(int(out_features), int(in_features), int(group), int(bool(zeros)))
+    n = 0
+    if 0 < out_features <= MAX_SIZE and 0 < in_features <= MAX_SIZE and 0 < group <= 128:  # (32 bits)
+        n = load_library().moe_w4_packed_bytes(int(out_features), int(in_features), int(group), int(bool(zeros)))
     if n == 0:
         raise ValueError(f"no packed form for [{out_features}, {in_features}] in groups of {group}")
     return n
@@ -130,6 +133,9 @@ def linear(x, packed, out, group: int, zeros: bool = False, bias=None, stream=No
                                       or not bias.is_contiguous()))):
         _refuse_linear(x, packed, out, group, zeros, bias)
     call = load_library().moe_w4_linear
+    # (numbers beyond 32 bits must not come around to small ones: the library refuses these)
+    if B > MAX_BATCH or K > MAX_SIZE or N > MAX_SIZE or group > 128:
+        B, K, N, group = MAX_BATCH + 1, 64, 1, 0
     args = (x.data_ptr(), packed.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), B, K, N, group,
             1 if zeros else 0, sx[0], so[0], code)
     if dev == _current_device():

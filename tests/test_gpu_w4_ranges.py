@@ -4,7 +4,7 @@ weights are rounded, half a step of each."""
 import pytest
 import torch
 
-from moe_decode_block_b200 import w4
+from moe_decode_block_b200 import MoEDecodeError, w4
 from gpu_helpers import margin_x
 from test_gpu_w4 import MANY, TINY_W4, W4Block, _check_linear, _x
 from w4_reference import TINY, U, assert_within, dequant64, product_magnitude, product_tolerance, random_w4
@@ -148,3 +148,13 @@ def test_block_from_the_definition(b, shape, group, zeros):
         m.check(x, out, ids, w)
     finally:
         blk.close()
+
+
+def test_a_number_of_tokens_beyond_32_bits_is_refused():
+    codes, scales, _ = random_w4(1, 64, 64, False, torch.bfloat16, seed=1)
+    packed, row = w4.pack(codes, scales), _x(1, 64, torch.bfloat16, seed=1)
+    out = torch.empty(2 ** 32 + 1, 1, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(MoEDecodeError):
+        w4.linear(row.expand(2 ** 32 + 1, 64), packed, out, 64)
+    del out
+    torch.cuda.empty_cache()

@@ -82,3 +82,22 @@ def test_wait_limit_and_hold_are_set_on_the_host():
         assert lib.moe_w4_linear_set_wait_limit(probes) == mdb.MOE_OK
     assert lib.moe_w4_test_hold(-1) == mdb.MOE_ERR_INVALID_ARG
     assert lib.moe_w4_test_hold(3) == mdb.MOE_OK and lib.moe_w4_test_hold(0) == mdb.MOE_OK
+
+
+def test_numbers_beyond_32_bits_do_not_come_around():
+    class Keeps:
+        def moe_decode_forward_w4(self, *args):
+            self.batch, self.group = args[10], args[11]
+            raise _Reached
+
+    blk = _handle()
+    blk._lib = Keeps()
+    for kw in (dict(group=2 ** 32 + 64), dict(group=48), dict(batch=1 - 2 ** 32)):
+        with pytest.raises(_Reached):
+            blk.forward_w4(**{**_args(), **kw})
+        assert blk._lib.group == (0 if "group" in kw else 64) and blk._lib.batch == (-1 if "batch" in kw else 3)
+    with pytest.raises(ValueError):
+        blk.forward_w4(**_args(), batch=2 ** 32 + 1)
+    for n, k, g in ((2 ** 32 + 16, 64, 64), (16, 2 ** 32 + 64, 64), (16, 64, 2 ** 32 + 64), (16, 64, -2 ** 32 + 64)):
+        with pytest.raises(ValueError):
+            w4.packed_bytes(n, k, g)
