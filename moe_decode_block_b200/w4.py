@@ -134,7 +134,7 @@ def linear(x, packed, out, group: int, zeros: bool = False, bias=None, stream=No
         _refuse_linear(x, packed, out, group, zeros, bias)
     call = load_library().moe_w4_linear
     # (numbers beyond 32 bits must not come around to small ones: the library refuses these)
-    if B > MAX_BATCH or K > MAX_SIZE or N > MAX_SIZE or group > 128:
+    if B > MAX_BATCH or K > MAX_SIZE or N > MAX_SIZE or not 0 < group <= 128:
         B, K, N, group = MAX_BATCH + 1, 64, 1, 0
     args = (x.data_ptr(), packed.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), B, K, N, group,
             1 if zeros else 0, sx[0], so[0], code)
