@@ -30,6 +30,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "moe_device.cuh"
 #include "moe_host.h"
 

@@ -23,6 +23,7 @@
 #pragma once
 
 #include "expert_mma.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 
@@ -40,20 +41,6 @@ __host__ __device__ inline size_t tc_extra_bytes() {
 __host__ __device__ inline size_t tc_smem_bytes(int n_stages) { return mma_smem_bytes(n_stages) + tc_extra_bytes(); }
 
 // ---- PTX wrappers (sm_100a) ------------------------------------------------
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst_smem)),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
 // D[tmem] (+)= A[smem desc] x B[smem desc], kind::f16, one CTA.
 __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -90,15 +77,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-
-// Shared-memory matrix descriptors (tcgen05): start address, leading and
-// stride byte offsets (all >> 4), descriptor version 1, layout type.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | ((uint64_t)layout << 61);
-}
-constexpr uint32_t kLayoutNone = 0;
-constexpr uint32_t kLayoutSw128 = 2;
 
 // Instruction descriptor, kind::f16: fp32 accumulate, bf16 A and B, A (the
 // weights) MN-major, B (the tokens) K-major, M = 128, N = n.

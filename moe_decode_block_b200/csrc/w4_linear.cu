@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kW4TcThreads, 1) w4_linear_tc_kernel(const __g
   static_assert(kW4TcThreads == 32 * 4 * (kTcTokens / 16), "a warp's quarter and tokens");
   const int c = 16 * (warp >> 2);
   if (c < a.batch && tc_wait(&bars.d_full[0], 0u, status, bars.ctl)) {
-    tc5_fence_after();
+    tc_fence_after();
     constexpr float unit = W4Dequant<T, ZP>::kUnit;
     const uint32_t d = bars.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c;
     float* to = exch + c * kTcRows + 32 * (warp & 3) + lane;

@@ -62,7 +62,10 @@
 // ended.
 #pragma once
 
+#include <type_traits>
+
 #include "moe_device.cuh"
+#include "tcgen05.cuh"
 #include "w4_core.cuh"
 
 namespace moe {
@@ -100,16 +103,6 @@ struct W4TcItem {
   __device__ __forceinline__ int steps() const { return (tile1 - tile0 + 1) / 2; }
 };
 
-__device__ __forceinline__ void tc5_alloc(uint32_t* dst, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tc5_dealloc(uint32_t addr, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
-}
-__device__ __forceinline__ void tc5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // 1 in one lane of the warp
 __device__ __forceinline__ uint32_t tc5_elect() {
   uint32_t r;
@@ -159,12 +152,6 @@ __device__ __forceinline__ void tc5_load16(uint32_t addr, float (&v)[16]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-// K-major operand without swizzle: cores of 8 rows x 16 bytes; lbo between cores
-// along K, sbo between groups of 8 rows.
-__device__ __forceinline__ uint64_t tc5_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 // fp32 sums, A and B of one 16-bit type, both K-major, M = 128
 template <typename T>
@@ -306,17 +293,20 @@ __device__ __forceinline__ void w4_tc_begin(W4TcBars& bars, int limit) {
     bars.ctl[1] = limit;
     mbar_fence_init();
   }
-  if (tid >> 5 == kTcMmaWarp) tc5_alloc(&bars.tmem, 512);
-  tc5_fence_before();
+  if (tid >> 5 == kTcMmaWarp) {
+    tmem_alloc(&bars.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
-  tc5_fence_after();
+  tc_fence_after();
 }
 // After them.
 __device__ __forceinline__ void w4_tc_end(W4TcBars& bars) {
-  tc5_fence_before();
+  tc_fence_before();
   __syncthreads();
-  tc5_fence_after();
-  if (threadIdx.x >> 5 == kTcMmaWarp) tc5_dealloc(bars.tmem, 512);
+  tc_fence_after();
+  if (threadIdx.x >> 5 == kTcMmaWarp) tmem_dealloc(bars.tmem, 512);
 }
 
 // The MMA warp.  `items` gives the CTA's items in order: next(item) is false
@@ -326,7 +316,9 @@ template <typename T, typename Items>
 __device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, Items items, int* status) {
   const uint32_t lead = tc5_elect();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0);
-  const uint64_t b_first = tc5_desc(smem_addr(smem + kTcB), kTcCore, kTcBGroup);
+  // K-major: cores of 8 tokens x 16 bytes, kTcCore apart along K, groups of 8 tokens
+  // kTcBGroup apart
+  const uint64_t b_first = smem_desc(smem_addr(smem + kTcB), kTcCore, kTcBGroup, kLayoutNone);
   uint32_t buf = 0, buf_phase = 0, slot = 0, slot_phase = 0, item = 0;
   bool ok = true;
   W4TcItem it;
@@ -338,7 +330,7 @@ __device__ __forceinline__ void w4_tc_mma(const uint8_t* smem, W4TcBars& bars, I
       ok = tc_wait(&bars.b_full[slot], slot_phase, status, bars.ctl) &&
            tc_wait(&bars.a_full[buf], buf_phase, status, bars.ctl);
       if (!ok) break;
-      tc5_fence_after();
+      tc_fence_after();
       const uint64_t b0 = b_first + (uint64_t)(slot * (uint32_t)(kTcBSlot >> 4));
       const uint32_t a = tmem + kTcOperandCol + buf * 128u;
       const uint32_t more = tile > it.tile0;
@@ -524,7 +516,7 @@ __device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Item
       ask(tile + 2);
       // the MMAs of two steps ago have read this buffer
       if (!(ok = tc_wait(&bars.a_empty[buf], buf_phase ^ 1u, status, bars.ctl))) break;
-      tc5_fence_after();
+      tc_fence_after();
       const uint32_t a = a0 + buf * 128u;
 #pragma unroll
       for (int ti = 0; ti < 2; ++ti) {
@@ -543,7 +535,7 @@ __device__ __forceinline__ void w4_tc_unpack(uint8_t* smem, W4TcBars& bars, Item
         slot = (slot + 2 * kW4TileBytes) % kTcRingBytes;
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      tc5_fence_before();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.a_full[buf]);
       if (++buf == kTcBufs) {
@@ -568,7 +560,7 @@ __device__ __forceinline__ void w4_tc_finish(W4TcBars& bars, Items items, int fi
   for (; items.next(it); ++item) {
     ready(items, it);
     if (!tc_wait(&bars.d_full[item & 1u], (item >> 1) & 1u, status, bars.ctl)) return;
-    tc5_fence_after();
+    tc_fence_after();
     const uint32_t d = bars.tmem + lanes + 128u * (item & 1u);
     for (int c = 0; c < it.n_tok; c += 16) {
       float lo[16], hi[16];
@@ -576,7 +568,7 @@ __device__ __forceinline__ void w4_tc_finish(W4TcBars& bars, Items items, int fi
       tc5_load16(d + 64u + c, hi);
       take(items, it, c, lo, hi);
     }
-    tc5_fence_before();
+    tc_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&bars.d_empty[item & 1u]);
   }
