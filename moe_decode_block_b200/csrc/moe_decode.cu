@@ -1024,8 +1024,9 @@ static __device__ __align__(256) uint8_t g_router_scratch[kNoAllocBytes];
 
 namespace {
 
-// First call on a device: resolve the scratch address, zero it once, read the
-// SM count.  Runs with `dev` current.
+// First call on a device: resolve the scratch address, read the SM count.  Runs
+// with `dev` current.  (The array is zero when it is loaded, and a call clears
+// what it needs so in its own stream.)
 int noalloc_setup(int dev, NoAllocDevice** out) {
   if (dev < 0 || dev >= kNoAllocMaxDevices) return MOE_ERR_NO_DEVICE;
   std::lock_guard<std::mutex> lock(g_noalloc_mu);
@@ -1037,7 +1038,6 @@ int noalloc_setup(int dev, NoAllocDevice** out) {
     if (major != 10) return MOE_ERR_ARCH;
     void* p = nullptr;
     if ((e = cudaGetSymbolAddress(&p, g_router_scratch)) != cudaSuccess) return fail_cuda(e);
-    if ((e = cudaMemset(p, 0, kNoAllocBytes)) != cudaSuccess) return fail_cuda(e);
     if ((e = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
       return fail_cuda(e);
     d.scratch = static_cast<uint8_t*>(p);
@@ -1156,7 +1156,9 @@ int moe_router_topk_noalloc_status(void* stream) {
   int st = 0;
   if ((e = cudaMemcpy(&st, scratch, sizeof st, cudaMemcpyDeviceToHost)) != cudaSuccess) return fail_cuda(e);
   if (st == moe::kStatusOk) return MOE_OK;
-  if ((e = cudaMemset(scratch, 0, sizeof st)) != cudaSuccess) return fail_cuda(e);
+  const cudaStream_t sm = static_cast<cudaStream_t>(stream);
+  if ((e = cudaMemsetAsync(scratch, 0, sizeof st, sm)) != cudaSuccess) return fail_cuda(e);
+  if ((e = cudaStreamSynchronize(sm)) != cudaSuccess) return fail_cuda(e);
   return st == moe::kStatusTimeout ? MOE_ERR_DEVICE_TIMEOUT : MOE_ERR_DEVICE_PLAN;
 }
 
@@ -1228,7 +1230,7 @@ int moe_decode_init(const moe_decode_shapes* shapes, moe_decode_t* out_handle) {
     cudaGetLastError();
     rc = MOE_ERR_OUT_OF_MEMORY;
   }
-  if (rc == MOE_OK && (e = cudaMemset(h->ws, 0, h->L.total)) != cudaSuccess) rc = fail_cuda(e);
+  if (rc == MOE_OK && (e = moe::host_zero_now(h->ws, h->L.total)) != cudaSuccess) rc = fail_cuda(e);
   if (rc == MOE_OK && (e = cudaEventCreateWithFlags(&h->ev_fork, cudaEventDisableTiming)) != cudaSuccess)
     rc = fail_cuda(e);
   if (rc == MOE_OK && (e = cudaEventCreateWithFlags(&h->ev_join, cudaEventDisableTiming)) != cudaSuccess)
@@ -1424,7 +1426,7 @@ int moe_decode_get_status(moe_decode_t h) {
   if (st == moe::kStatusOk) return MOE_OK;
   // The workspace may be inconsistent after a device-side failure: clear
   // the status now and re-zero everything at the next forward.
-  if ((e = cudaMemset(dst, 0, sizeof(int))) != cudaSuccess) return fail_cuda(e);
+  if ((e = moe::host_zero_now(dst, sizeof(int))) != cudaSuccess) return fail_cuda(e);
   h->dirty = true;
   return st == moe::kStatusTimeout ? MOE_ERR_DEVICE_TIMEOUT : MOE_ERR_DEVICE_PLAN;
 }

@@ -13,6 +13,20 @@ namespace moe {
 // Record a CUDA error for moe_decode_last_cuda_error; returns MOE_ERR_CUDA.
 int host_fail_cuda(cudaError_t e);
 
+// Set device memory to zero before returning.  (cudaMemset returns early, and
+// its stream, the legacy default one, is not waited for by streams made with
+// cudaStreamNonBlocking, as torch's are: behind other work it could come after
+// kernels that need the zeros, or under them.)
+inline cudaError_t host_zero_now(void* p, size_t bytes) {
+  cudaStream_t st = nullptr;
+  cudaError_t e = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(p, 0, bytes, st);
+  const cudaError_t s = cudaStreamSynchronize(st);
+  cudaStreamDestroy(st);
+  return e != cudaSuccess ? e : s;
+}
+
 inline bool host_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 constexpr int kHostMaxDevices = 64;

@@ -501,8 +501,12 @@ int moe_w4_linear_status(void* stream) {
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&st, g_w4_linear_status, sizeof st);
   if (e != cudaSuccess) return host_fail_cuda(e);
   if (st == kStatusOk) return MOE_OK;
-  const int zero = kStatusOk;
-  if ((e = cudaMemcpyToSymbol(g_w4_linear_status, &zero, sizeof zero)) != cudaSuccess) return host_fail_cuda(e);
+  static_assert(kStatusOk == 0, "cleared to zero");
+  void* word = nullptr;
+  if ((e = cudaGetSymbolAddress(&word, g_w4_linear_status)) != cudaSuccess ||
+      (e = cudaMemsetAsync(word, 0, sizeof st, static_cast<cudaStream_t>(stream))) != cudaSuccess ||
+      (e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream))) != cudaSuccess)
+    return host_fail_cuda(e);
   return MOE_ERR_DEVICE_TIMEOUT;
 }
 
