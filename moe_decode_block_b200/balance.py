@@ -48,7 +48,8 @@ def balance_loss(logits, topk_ids, loss, counts, token_mask=None, router_bias=No
     gradient, times grad_loss [1].  token_mask [T] bool or uint8: 0 is a padded
     token.  workspace (above ONE_LAUNCH tokens): a uint8 tensor of
     workspace_bytes(E), by default a new one (torch's allocator ties it to the
-    current stream, so pass one when `stream` is another)."""
+    current stream, so pass one when `stream` is another).  Autograd does not
+    see the call: dlogits is the gradient."""
     T, E = logits.shape
     Ti, k = topk_ids.shape
     dev = logits.get_device()

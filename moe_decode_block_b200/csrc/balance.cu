@@ -21,11 +21,13 @@
 // fixed order (no atomics on floats), so every call gives the same bits.
 //
 // What bounds it: HBM -- the logits once, and the gradient once: 65,536 tokens of
-// 384 experts in fp32 with the gradient in 44 us, 4.6 TB/s (the row kernel alone 40
-// us), below the copy rate for the counting that comes first.  Few tokens are
-// bound by latency, so up to 512 tokens one cluster does all of it in one launch:
-// 5.9 us at 64 tokens, 8.9 at 512 (10.0 with the gradient), where the two kernels
-// of more tokens take 10.3 us from 513 to 2,048.
+// 384 experts in fp32 with the gradient in 44 us, 4.6 TB/s (by a profiler the row
+// kernel takes 34 us of it and the counting before it 8, most of that in the open);
+// without the gradient 27 us, in bf16 with it 35.  Few tokens are bound by latency,
+// so up to 512 tokens one cluster does all of it in one launch: 5.5 us at 64
+// tokens, 7.9 at 512 (5.9 and 8.9 with the gradient), where the memset and two
+// kernels of more tokens take 10.3 us from 513 to 2,048.  (385 to 512 experts
+// spill 40 to 48 bytes a thread at the 64 registers of two CTAs on an SM.)
 #include <cooperative_groups.h>
 
 #include <cuda_fp16.h>

@@ -30,10 +30,13 @@
 // turns into the four A registers of m16n8k16 by masks, while the lane's B
 // registers are 16 contiguous bytes of x.
 //
-// What bounds it.  HBM for large matrices up to 16 tokens, and not far behind it
-// the ALU pipe: 5 of its instructions for 8 codes, two cycles each, are 40 of
-// the 88 cycles that a scheduler has for 1,024 weights at HBM's rate (46 weights
-// a clock and SM).  (Subtracting the zero point from every operand, with its
+// What bounds it.  With one token tile HBM comes first -- 16,384 x 7,168 at one
+// token in 13.2 us, 4.6 TB/s -- and not far behind it the ALU pipe: 5 of its
+// instructions for 8 codes, two cycles each, are 40 of the 88 cycles that a
+// scheduler has for 1,024 weights at HBM's rate (46 weights a clock and SM; in the
+// experts of a full-size block of 8 tokens it is busy 54 % of the time, HBM 63 %,
+// the tensor pipe 37 %, and a warp's longest wait is for its own dependent
+// instructions).  With two token tiles neither is: see w4_linear_kernel.  (Subtracting the zero point from every operand, with its
 // shifts, took 28 ALU and 16 more instructions for 1,024 codes instead of 20,
 // and held the kernel to 40 weights a clock.)  So everything else is kept off
 // the issue slots: a step of a warp is a pair of tiles (128 inputs) of 4 panels,

@@ -21,14 +21,20 @@
 // kernel of the same two projections (w4_tc.cuh, items of 256 weight rows), beside
 // which the first kind runs.  With mma.sync up to 16 tokens (two token tiles, 128
 // registers and 220 to 450 bytes of spills) the full-size block took 626 us
-// instead of 519 at 16 tokens, the block of 16 experts 181 instead of 138.
+// instead of 519 at 16 tokens, the block of 16 experts 181 instead of 138.  (The
+// rule is measured with experts of 7,168 x 2,048 only.  What it costs a batch of 9
+// is three launches and the shared expert no longer under the router: 339 us where
+// 8 tokens take 270 for the full-size block, 31 against 22 for a block of 256 x
+// 128, whose work is a tenth of a microsecond.)
 //
 // What bounds it.  The full-size block: HBM at 8 tokens (64 experts, zero points:
-// 283 us, 5 TB/s), the router's 15 us and the latency of short kernels at one
-// token (61 us).  16 experts at 64 tokens: 182 us, of which the router takes 34,
+// 276 us, 5.2 TB/s), the router's 15 us and the latency of short kernels at one
+// token (60 us); at 16, 32 and 64 tokens 500, 813 and 1,267 us for 391, 667 and
+// 1,005 of bytes.  16 experts at 64 tokens: 179 us, of which the router takes 34,
 // the up projection 85 and the down projection 55: steps of w4_tc.cuh, and a last
 // wave of items that fills the GPU in part (272 items of the up projection on 148
-// SMs, 476 of the down projection).
+// SMs, 476 of the down projection).  Registers: 128 with 8 to 104 bytes of spills
+// in w4_expert_kernel, 116 to 121 without in the tcgen05 kernel.
 #pragma once
 
 #include "moe_device.cuh"

@@ -34,11 +34,15 @@ struct W4LinearArgs {
 // order: warps first, then the cluster's CTAs through distributed shared
 // memory.  Nothing is kept in global memory between calls.
 //
-// Measured (device time, weights from HBM): 4,096 x 7,168 at one token 6.3 us (2.4
-// TB/s), 7,168 x 2,048 at 8 tokens with zero points 5.3 us, 256 x 256 2.7 us -- the
+// Measured (device time, weights from HBM): 4,096 x 7,168 at one token 5.7 us (2.6
+// TB/s), 7,168 x 2,048 at 8 tokens with zero points 5.1 us, 256 x 256 2.4 us -- the
 // latency of a launch, one trip to HBM and the cluster's exchange bounds them; a
-// call from Python costs the host 6.8 us.  16,384 x 7,168 at 16 tokens: 23 us, 2.6
-// TB/s, the tensor pipe (976 products a clock and SM).
+// call from Python costs the host 7 us.  16,384 x 7,168: 13.2 us at one token (4.6
+// TB/s), 14.1 at 8.  At 16 tokens 23.6 us, 2.6 TB/s, and no pipe is full (tensor 40
+// %, ALU 28 %): two token tiles take 128 registers and spill 4 to 136 bytes, so
+// there are 3.4 warps to a scheduler (256 CTAs in 296 places), each of which issues
+// every 9 cycles, waiting for loads of x and weights a third of that and mostly for
+// its own dependent MMAs otherwise.
 template <typename T, int NT, int GROUP, bool ZP>
 __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kMinCtas)
     w4_linear_kernel(const __grid_constant__ W4LinearArgs a) {
@@ -131,7 +135,11 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
 }
 
 // More than 16 tokens: 256 outputs x up to 64 tokens on tcgen05 (w4_tc.cuh); the
-// CTAs of a cluster split K as above.  16,384 x 7,168 at 64 tokens: 27 us.  (With
+// CTAs of a cluster split K as above.  (The other kernel is faster at every size up
+// to 16 tokens: 4.1 against 6.3 us for 256 x 1,024, 10.1 against 14.1 for 4,096 x
+// 7,168, 23.4 against 23.5 for 16,384 x 7,168; two of its calls of 16 tokens are
+// slower than one of 32 here: 8.1 against 6.6, 20 against 14.8, 47 against 24.5.)
+//  16,384 x 7,168 at 64 tokens: 27 us.  (With
 // the sums read by four warps, and each thread waiting for one remote value after
 // another, 31 us.)  4,096 x 7,168 at 32 tokens: 14.7 us.
 template <typename T>

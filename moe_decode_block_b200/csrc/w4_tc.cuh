@@ -7,10 +7,9 @@
 // 16 weights a clock and SM where HBM delivers 46.  tcgen05.mma takes all tokens
 // at once: 128 weight rows x up to 64 tokens x 16 inputs in 45 to 52 clocks
 // (measured, the same for 16, 32 and 64 tokens; the weights in tensor memory), 40
-// to 45 weights a clock.  A layer of 16,384 x 7,168 takes 23 us at 9 to 16 tokens
-// with mma.sync (two token tiles), 24.5 at 17 to 32 and 27 at 64 here: the dense
-// layer changes over above 16 tokens.  In the block, whose two-tile mma.sync
-// instance spilled, the change comes above 8 (w4_experts.cuh).
+// to 45 weights a clock.  The dense layer changes over above 16 tokens, the block's
+// experts above 8; both sides are measured at w4_linear_tc_kernel and in
+// w4_experts.cuh.
 //
 // Mathematics.  Here a weight s (q - z) is rounded once to the activations' type
 // (half a step: up to 2^-8 of it in bf16, 2^-11 in fp16; it has to fit the type)
