@@ -357,8 +357,8 @@ int moe_w4_pack(const void* codes, const void* scales, const void* zeros, void* 
  * and sums in fp32, one rounding to the type of x in the end.  Up to 16 tokens
  * no weight is rounded; above, each weight s (q - z) is rounded once to the type
  * of x, which has to hold it; in bf16 scales are then below 2^27 (2^122 with zero
- * points).  An infinite activation may give NaN; |x| in bf16 is held from 2^-57 to
- * 2^63 up to 16 tokens.
+ * points).  An infinite activation may give NaN; in bf16, up to 16 tokens, |x| is
+ * held from 2^-57 to 2^63 and a sum to within 2^-72, if not better.
  * Deterministic.  Asynchronous on `stream` of the current device, one kernel,
  * no workspace, nothing kept between calls: calls may overlap on any streams
  * and be captured in CUDA graphs.

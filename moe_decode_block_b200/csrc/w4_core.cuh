@@ -17,7 +17,8 @@
 // So an operand register costs one mask, and every second one no shift.  The
 // powers of two come off in the end; bf16 activations are multiplied by 2^64 on
 // their way in (exact) so that their products with 2^-133 stay normal fp32
-// numbers: |x| is held from 2^-57 to 2^63.  An infinite activation gives NaN
+// numbers: |x| is held from 2^-57 to 2^63, and the scaled sums, in units of 2^-69,
+// to within 2^-80 an addition.  An infinite activation gives NaN
 // (infinity minus infinity), as do sums beyond fp32.
 //
 // Layout (moe_w4_pack).  A matrix is stored as panels of 16 outputs; a panel is

@@ -135,13 +135,13 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT, GROUP, ZP, kW4Warps>::kM
 }
 
 // More than 16 tokens: 256 outputs x up to 64 tokens on tcgen05 (w4_tc.cuh); the
-// CTAs of a cluster split K as above.  (The other kernel is faster at every size up
-// to 16 tokens: 4.1 against 6.3 us for 256 x 1,024, 10.1 against 14.1 for 4,096 x
-// 7,168, 23.4 against 23.5 for 16,384 x 7,168; two of its calls of 16 tokens are
-// slower than one of 32 here: 8.1 against 6.6, 20 against 14.8, 47 against 24.5.)
-//  16,384 x 7,168 at 64 tokens: 27 us.  (With
+// CTAs of a cluster split K as above.  16,384 x 7,168 at 64 tokens: 27 us.  (With
 // the sums read by four warps, and each thread waiting for one remote value after
-// another, 31 us.)  4,096 x 7,168 at 32 tokens: 14.7 us.
+// another, 31 us.)  4,096 x 7,168 at 32 tokens: 14.8 us.  The other kernel is faster
+// at every size up to 16 tokens (4.1 against 6.3 us for 256 x 1,024, 10.1 against
+// 14.1 for 4,096 x 7,168, 23.4 against 23.5 for 16,384 x 7,168), and two of its
+// calls of 16 tokens are slower than one of 32 here: 8.1 against 6.6, 20 against
+// 14.8, 47 against 24.5.
 template <typename T>
 struct W4LinearItems {
   const W4LinearArgs& a;

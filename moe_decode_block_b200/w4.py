@@ -115,8 +115,9 @@ def linear(x, packed, out, group: int, zeros: bool = False, bias=None, stream=No
     [N] or None; all of one 16-bit type; no row of out on a row of x.  `stream`
     belongs to x's device.
 
-    Sums in fp32.  Up to 16 tokens no weight is rounded; |x| in bfloat16 is
-    held from 2^-57 to 2^63 and an infinite activation gives NaN.  Above 16
+    Sums in fp32.  Up to 16 tokens no weight is rounded; in bfloat16 |x| is
+    held from 2^-57 to 2^63 and a sum to within 2^-72, if not better, and an
+    infinite activation gives NaN.  Above 16
     each weight s (q - z) is rounded once to x's type, which has to hold it;
     scales in bfloat16 are then below 2^27 (2^122 with zero points)."""
     B, K = x.shape
