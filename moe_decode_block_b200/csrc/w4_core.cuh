@@ -244,9 +244,10 @@ __device__ __forceinline__ void w4_stream_step(W4Stream& st, uint32_t slot, int 
     const int m = lane / C::kChunks;
     if (C::kPieces >= 32 || lane < C::kPieces) {
       cp_async_16(dst + C::kCodes, in ? st.entry : st.code, in && (!CHECK || ((st.valid >> m) & 1u)));
-      if constexpr (C::kPieces > 32)
-        cp_async_16(dst + C::kCodes + 512, in ? st.entry + st.entry2 : st.code,
-                    in && (!CHECK || ((st.valid >> (m + 2)) & 1u)));
+      if constexpr (C::kPieces > 32) {
+        const bool v = in && (!CHECK || ((st.valid >> (m + 2)) & 1u));
+        cp_async_16(dst + C::kCodes + 512, v ? st.entry + st.entry2 : st.code, v);  // (entry2 is of panels that exist)
+      }
     }
   }
   st.code += 2 * kW4TileBytes;
